@@ -322,6 +322,107 @@ SVDQ_API svdq_status svdq_deltaquant_sizes(int64_t F, int64_t H, int64_t W, int6
 SVDQ_API svdq_status svdq_deltaquant_encode(int64_t F, int64_t H, int64_t W, int64_t C, const void* X, void* core,
                                             void* Qd, void* Sd, void* stream);
 
+/* ------------------------------------------------ around the 4-bit linear layer
+ * The operators that stand beside it in a transformer block: the 8-bit (W8A8)
+ * linear layer for projections that 4 bits do not suit, layer norm (plain or
+ * modulated, with its gradient, or with the 8-bit quantizer behind it) and
+ * rotary positions over several axes. They take bf16, fp16 or fp32 and allow
+ * row strides; the conventions above hold otherwise (device pointers aligned to
+ * 16 bytes, caller-owned memory, asynchronous on `stream`). Each reads its
+ * inputs and writes its outputs within the call's work on the stream; calls
+ * with buffers of their own may run at once on several streams. An output may
+ * be an input's memory only where that is said.
+ */
+typedef enum { SVDQ_BF16 = 0, SVDQ_FP16 = 1, SVDQ_FP32 = 2, SVDQ_INT32 = 3 } svdq_dtype;
+
+/* 8-bit codes of the rows of X [M][K] (type x_dtype: SVDQ_BF16, _FP16 or
+ * _FP32; row stride ldx >= K in elements, a multiple of 16 bytes when M > 1),
+ * one scale per row:
+ *   v = fp32(x * inv_lambda[k])   (inv_lambda fp32 [K], or NULL: v = x)
+ *   s = fp32(max|v| / 127),  q = clamp(RNE(v / s), -127, 127) of the exact
+ *   quotient (ties to even); all 0 if s == 0. A row with an infinity or a NaN
+ *   gets the scale NaN and codes 0: what is computed from it is NaN.
+ * Writes Qx int8 [M][K] and Sx fp32 [M]. K a multiple of 16, 16 <= K <= 131072.
+ * (walkthrough eq. (1) with q_max = 127; handbook, Quantization chapter, W8A8.) */
+SVDQ_API svdq_status svdq_int8_quantize_act(int64_t M, int64_t K, int x_dtype, const void* X, int64_t ldx,
+                                            const float* inv_lambda, void* Qx, float* Sx, void* stream);
+
+/* The same codes for the rows of W_lin [N][K] (one scale per output channel),
+ * with the smoothing factor multiplied in: v = fp32(w * lambda[k]). */
+SVDQ_API svdq_status svdq_int8_quantize_weight(int64_t N, int64_t K, int w_dtype, const void* W_lin, int64_t ldw,
+                                               const float* lambda, void* Qw, float* Sw, void* stream);
+
+/* Y[m][n] = Sx[m] Sw[n] sum_k Qx[m][k] Qw[n][k] + bias[n]: the integer sum is
+ * exact; it is rounded to fp32, multiplied by Sw and then Sx, the bias (fp32
+ * [N], or NULL) is added with one rounding, and Y (type y_dtype, row stride
+ * ldy >= N) takes the result rounded once. Any M >= 0 and N >= 1 (up to 2^24);
+ * codes in [-127, 127] (-128 too); K as above. No workspace. */
+SVDQ_API svdq_status svdq_int8_linear(int64_t M, int64_t K, int64_t N, const void* Qx, const float* Sx,
+                                      const void* Qw, const float* Sw, const float* bias, int y_dtype, void* Y,
+                                      int64_t ldy, void* stream);
+
+#define SVDQ_NORM_ADD_ONE 1u   /* the weight is 1 + weight (a modulation scale), added in fp32 */
+
+/* Layer norm of the rows of X [M][C] (type dtype, row stride ldx >= C):
+ *   mean, var = mean and variance (divisor C) of the row, rstd = 1/sqrt(var + eps)
+ *   Y[m][c] = (X[m][c] - mean) rstd w[g][c] + b[g][c],  g = m / rows_per_group
+ * in fp32, rounded once. weight and bias [groups][C] have the type of X or fp32
+ * (w_dtype) and may each be NULL (1 and 0; NULL weight with SVDQ_NORM_ADD_ONE is
+ * 1 as well). rows_per_group = 0: one group for all rows, the affine norm; else
+ * groups = ceil(M / rows_per_group), as for the modulated norm of a batch of
+ * images with a scale and a shift each. mean and rstd fp32 [M] are written if
+ * non-NULL (the backward pass wants them). 1 <= C <= 16384, any C; multiples of
+ * 16 bytes run faster. eps >= 0. Y may be X (then ldy == ldx). */
+SVDQ_API svdq_status svdq_layernorm(int64_t M, int64_t C, int dtype, int w_dtype, const void* X, int64_t ldx,
+                                    const void* weight, const void* bias, int64_t rows_per_group, float eps,
+                                    unsigned int flags, void* Y, int64_t ldy, float* mean, float* rstd, void* stream);
+
+/* svdq_layernorm whose rows go straight to svdq_int8_quantize_act's codes and
+ * scales, without the rounding of Y to 16 bits and without Y in memory:
+ * v = fp32(y * inv_lambda[c]) of the fp32 y. C a multiple of 16. */
+SVDQ_API svdq_status svdq_int8_layernorm_quantize(int64_t M, int64_t C, int dtype, int w_dtype, const void* X,
+                                                  int64_t ldx, const void* weight, const void* bias,
+                                                  int64_t rows_per_group, float eps, unsigned int flags,
+                                                  const float* inv_lambda, void* Qx, float* Sx, void* stream);
+
+/* Gradients of svdq_layernorm. With h = dY w and xhat = (X - mean) rstd:
+ *   dX = rstd (h - mean_c(h) - xhat mean_c(h xhat))   (type dtype)
+ *   dweight[g] = sum over the group's rows of dY xhat, dbias[g] = sum of dY
+ * dweight and dbias are fp32 [groups][C], summed in fp32 in a fixed order (two
+ * calls give the same bits), and may each be NULL. mean and rstd are those of
+ * the forward pass. M = 0 writes zeros to dweight and dbias [1][C]. dX may be dY
+ * or X (with its row stride). The workspace holds partial sums:
+ * svdq_layernorm_backward_workspace() bytes, NULL when that is 0 or dweight and
+ * dbias are both NULL; it must not be shared by calls that overlap. */
+SVDQ_API svdq_status svdq_layernorm_backward_workspace(int64_t M, int64_t C, int64_t rows_per_group, size_t* bytes);
+SVDQ_API svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype, const void* dY,
+                                             int64_t lddy, const void* X, int64_t ldx, const void* weight,
+                                             const float* mean, const float* rstd, int64_t rows_per_group,
+                                             unsigned int flags, void* dX, int64_t lddx, float* dweight,
+                                             float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+#define SVDQ_ROPE_HALVES 1u    /* pair i is elements (i, i + R/2); default: (2i, 2i + 1) */
+#define SVDQ_ROPE_INVERSE 2u   /* turn by the opposite angle: the gradient of the rotation */
+
+/* Rotary positions over several axes (time, height, width, ...). The first
+ * R = sum(axis_dims) elements of each head form R/2 pairs; the pairs are dealt
+ * to the axes in order, axis_dims[a] / 2 to axis a. Pair i of token t turns by
+ * positions[t % pos_rows][axis(i)] * freqs[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * and elements past R are copied. X and Y [T][heads][D] of type dtype with any
+ * token and head strides (in elements; elements of a head are contiguous): the
+ * query and key heads inside a merged QKV activation, or heads ahead of tokens.
+ * Heads of X may overlap or repeat (stride 0), heads of Y may not. Y may be X
+ * with the same strides. positions [pos_rows][axes], int32 or fp32 (pos_dtype),
+ * T a multiple of pos_rows (a batch may share its positions); freqs fp64 [R/2]
+ * on the device; axis_dims [axes] on the host, each even and >= 2, 1 to 8 axes,
+ * R <= D <= 512. Angles are formed and reduced in fp64, so far positions keep
+ * their precision; the turn is in fp32, rounded once. */
+SVDQ_API svdq_status svdq_rope(int64_t T, int32_t heads, int32_t D, int dtype, const void* X, int64_t x_token_stride,
+                               int64_t x_head_stride, void* Y, int64_t y_token_stride, int64_t y_head_stride,
+                               const void* positions, int pos_dtype, int64_t pos_rows, int32_t axes,
+                               const int32_t* axis_dims, const double* freqs, unsigned int flags, void* stream);
+
 /* Diagnostic of the failure path (the pages have no counterpart): one thread
  * waits, with the library's bounded wait, on a barrier phase that nothing
  * completes; after the wait limit (2 s) it records the device error word and

@@ -1,0 +1,196 @@
+"""Layer norm on the GPU: forward, backward and the form that ends in 8-bit
+codes, against the 64-bit oracle within counted roundings."""
+import numpy as np
+import pytest
+import torch
+
+import block_oracle as B
+from w4a4_diffusion_model_b200 import svdq as S
+
+pytestmark = pytest.mark.gpu
+BF, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.fail("the gpu tests need a CUDA device")
+    S.load()
+
+
+def case(M, C, dtype, wtype, groups, seed=0, rows=None):
+    g = torch.Generator().manual_seed(seed + 31 * M + C)
+    x = torch.randn(M, C, generator=g) * torch.exp(0.5 * torch.randn(C, generator=g)) + 0.5 * torch.randn(C, generator=g)
+    shape = (C,) if groups is None else (groups, C)
+    w = torch.randn(shape, generator=g) * 0.5 + 0.5
+    b = torch.randn(shape, generator=g)
+    dy = torch.randn(M, C, generator=g)
+    return x.to(dtype), w.to(wtype), b.to(wtype), dy.to(dtype)
+
+
+def run(x, w, b, dy, rows=None, add_one=False, eps=1e-6):
+    dtype = x.dtype
+    c = lambda t: None if t is None else t.cuda()  # noqa: E731
+    X, W, Bb, dY = c(x), c(w), c(b), c(dy)
+    Y, mean, rstd = S.svdq_layernorm(X, W, Bb, eps, rows, add_one)
+    M, C = x.shape
+    n = 0 if w is None or w.dim() == 1 else rows or M // w.shape[0]
+    n64 = lambda t: None if t is None else B.np64(t)  # noqa: E731
+    y, mu, r, by, bmu, br = B.layernorm(B.np64(x), n64(w), n64(b), eps, n, add_one)
+    B.within(mean, mu, bmu + B.U * np.abs(mu) + 2.0 ** -140, "mean")
+    B.within(rstd, r, br + B.U * r, "rstd")
+    B.within(Y, y, by + B.rounding(y, dtype), "Y")
+    dX, dw, db = S.svdq_layernorm_backward(dY, X, W, mean, rstd, rows, add_one)
+    dx, gw, gb, bx, bw, bb = B.layernorm_backward(B.np64(dy), B.np64(x), n64(w), B.np64(mean), B.np64(rstd), n, add_one)
+    B.within(dX, dx, bx + B.rounding(dx, dtype), "dX")
+    shape = (C,) if w is None else w.shape
+    assert dw.shape == shape and db.shape == shape
+    B.within(dw, gw.reshape(shape), bw.reshape(shape) + B.rounding(gw.reshape(shape), FP32), "dweight")
+    B.within(db, gb.reshape(shape), bb.reshape(shape) + B.rounding(gb.reshape(shape), FP32), "dbias")
+    return Y, mean, rstd, dX, dw, db
+
+
+# widths of one value, below and above a warp, ragged, of several vectors, the largest; rows from one up
+@pytest.mark.parametrize("M,C", [(1, 1), (5, 3), (3, 8), (33, 64), (2, 255), (10, 1152), (37, 1151), (4, 2048),
+                                 (19, 2050), (6, 4096), (3, 5120), (2, 8192), (2, 16384), (2, 16383), (700, 96),
+                                 (1301, 40)])
+@pytest.mark.parametrize("dtype,wtype", [(BF, BF), (BF, FP32), (FP16, FP16), (FP16, FP32), (FP32, FP32)])
+def test_affine(M, C, dtype, wtype):
+    run(*case(M, C, dtype, wtype, None))
+
+
+@pytest.mark.parametrize("M,C,groups,rows", [(8, 64, 2, None), (600, 256, 3, None), (7, 48, 7, None),
+                                             (10, 32, 3, 4), (9, 33, 2, 8), (2000, 128, 2, None), (300, 16, 300, None)])
+@pytest.mark.parametrize("add_one", [False, True])
+def test_modulated_groups(M, C, groups, rows, add_one):
+    for dtype, wtype in ((BF, BF), (FP32, FP32), (FP16, FP32)):
+        run(*case(M, C, dtype, wtype, groups), rows=rows, add_one=add_one)
+
+
+def test_without_weight_or_bias():
+    x, w, b, dy = case(12, 136, BF, BF, None)
+    run(x, None, None, dy)
+    run(x, w, None, dy)
+    Y, *_ = S.svdq_layernorm(x.cuda(), None, b.cuda())
+    y, *_, = B.layernorm(B.np64(x), None, B.np64(b), 1e-6, 0, False)
+    by = B.layernorm(B.np64(x), None, B.np64(b), 1e-6, 0, False)[3]
+    B.within(Y, y, by + B.rounding(y, BF))
+
+
+def test_rows_with_large_means_and_constant_rows():
+    """The variance is taken around the mean: a mean of 1000 deviations costs no more than its bound, a constant row
+    has variance 0 and a finite gradient."""
+    x, w, b, dy = case(6, 512, FP32, FP32, None)
+    x[0] += 1000
+    x[1] = 3.0
+    x[2] = 0.0
+    Y, mean, rstd, dX, *_ = run(x, w, b, dy, eps=1e-5)
+    assert torch.equal(Y[1:3].cpu(), b.expand(2, -1)) and torch.isfinite(dX).all()
+
+
+def test_nan_and_infinity_stay_in_their_rows():
+    x, w, b, dy = case(5, 200, FP32, FP32, None)
+    clean = S.svdq_layernorm(x.cuda(), w.cuda(), b.cuda())[0]
+    x[1, 3], x[3, 199] = float("nan"), float("inf")
+    Y = S.svdq_layernorm(x.cuda(), w.cuda(), b.cuda())[0]
+    assert torch.isnan(Y[1]).all() and torch.isnan(Y[3]).any()
+    assert torch.equal(Y[[0, 2, 4]], clean[[0, 2, 4]])
+
+
+@pytest.mark.parametrize("C,pad", [(64, 8), (64, 3), (1152, 16), (130, 1)])
+def test_strided_rows_and_in_place(C, pad):
+    x, w, b, dy = case(21, C, BF, BF, None)
+    Y, mean, rstd = S.svdq_layernorm(x.cuda(), w.cuda(), b.cuda())
+    dX, dw, db = S.svdq_layernorm_backward(dy.cuda(), x.cuda(), w.cuda(), mean, rstd)
+    wide = torch.full((21, C + pad), 5.0, dtype=BF, device="cuda")
+    X = wide[:, :C]
+    X.copy_(x)
+    assert torch.equal(S.svdq_layernorm(X, w.cuda(), b.cuda())[0], Y)
+    grad = torch.full((21, C + pad), 5.0, dtype=BF, device="cuda")
+    G = grad[:, :C]
+    G.copy_(dy)
+    got = S.svdq_layernorm_backward(G, X, w.cuda(), mean, rstd, out=G)
+    assert torch.equal(G, dX) and torch.allclose(got[1], dw, rtol=1e-5, atol=1e-5)
+    S.svdq_layernorm(X, w.cuda(), b.cuda(), out=X)
+    assert torch.equal(X, Y) and (wide[:, C:] == 5).all() and (grad[:, C:] == 5).all()
+
+
+def test_no_rows():
+    x = torch.empty(0, 64, dtype=BF, device="cuda")
+    w = torch.ones(64, dtype=BF, device="cuda")
+    Y, mean, rstd = S.svdq_layernorm(x, w)
+    dX, dw, db = S.svdq_layernorm_backward(Y, x, w, mean, rstd)
+    assert Y.shape == dX.shape == (0, 64) and not dw.any() and not db.any() and dw.shape == (64,)
+
+
+def test_two_calls_give_the_same_bits():
+    x, w, b, dy = (t.cuda() for t in case(3000, 384, BF, FP32, 3))
+    _, mean, rstd = S.svdq_layernorm(x, w, b)
+    first = S.svdq_layernorm_backward(dy, x, w, mean, rstd)
+    for _ in range(3):
+        for a, c in zip(first, S.svdq_layernorm_backward(dy, x, w, mean, rstd)):
+            assert torch.equal(a, c)
+
+
+def test_gradient_against_differences():
+    """dX, dweight and dbias of sum(Y * dY) against central differences of the forward pass in fp64."""
+    x, w, b, dy = case(4, 24, FP32, FP32, 2)
+    eps = 1e-6
+    _, mean, rstd = S.svdq_layernorm(x.cuda(), w.cuda(), b.cuda(), eps, add_one=True)
+    dX, dw, db = S.svdq_layernorm_backward(dy.cuda(), x.cuda(), w.cuda(), mean, rstd, add_one=True)
+
+    def loss(xx, ww, bb):
+        return (B.layernorm(xx, ww, bb, eps, 2, True)[0] * B.np64(dy)).sum()
+
+    args = [B.np64(x), B.np64(w), B.np64(b)]
+    step = 1e-5
+    for k, got in enumerate((dX, dw, db)):
+        num = np.zeros_like(args[k])
+        for i in np.ndindex(num.shape):
+            hi, lo = [a.copy() for a in args], [a.copy() for a in args]
+            hi[k][i] += step
+            lo[k][i] -= step
+            num[i] = (loss(*hi) - loss(*lo)) / (2 * step)
+        # truncation step^2 f''' / 6 and cancellation 2^-52 |loss| / step, both far below 1e-5; fp32 adds its steps
+        np.testing.assert_allclose(B.np64(got), num, rtol=1e-4, atol=1e-4)
+
+
+@pytest.mark.parametrize("M,C", [(1, 16), (9, 1152), (300, 2048), (5, 5120), (3, 16384)])
+@pytest.mark.parametrize("dtype", [BF, FP16, FP32])
+def test_norm_into_codes(M, C, dtype):
+    """Scales within the norm's roundings; a code off by one only where the exact quotient is that near a midpoint."""
+    x, w, b, _ = case(M, C, dtype, dtype, 1)
+    lam = torch.exp(0.3 * torch.randn(C, generator=torch.Generator().manual_seed(C)))
+    Q, s = S.svdq_int8_layernorm_quantize(x.cuda(), w.cuda(), b.cuda(), lam.cuda(), add_one=True)
+    y, *_, = B.layernorm(B.np64(x), B.np64(w), B.np64(b), 1e-6, 0, True)
+    by = B.layernorm(B.np64(x), B.np64(w), B.np64(b), 1e-6, 0, True)[3]
+    v, bv = y * B.np64(lam), by * B.np64(lam) + B.U * np.abs(y * B.np64(lam))
+    top = np.abs(v).max(1)
+    B.within(s, top / 127, bv.max(1) / 127 + 2 * B.U * top / 127, "scale")
+    sg = B.np64(s)[:, None]
+    # |code - v / s| is half a step, and what v and the quotient's own settling may be off
+    B.within(Q.double(), v / sg, 0.5 + bv / sg + 1e-9, "codes")
+
+
+def test_norm_into_codes_matches_the_two_calls_in_fp32():
+    x, w, b, _ = case(50, 768, FP32, FP32, None)
+    Y, *_ = S.svdq_layernorm(x.cuda(), w.cuda(), b.cuda())
+    Q2, s2 = S.svdq_int8_quantize_act(Y)
+    Q, s = S.svdq_int8_layernorm_quantize(x.cuda(), w.cuda(), b.cuda())
+    assert torch.equal(Q, Q2) and torch.equal(s, s2)      # fp32 Y has nothing to lose
+
+
+def test_captured_backward():
+    x, w, b, dy = (t.cuda() for t in case(500, 256, BF, BF, 2))
+    _, mean, rstd = S.svdq_layernorm(x, w, b)
+    S.svdq_layernorm_backward(dy, x, w, mean, rstd)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Y, mean, rstd = S.svdq_layernorm(x, w, b)
+        out = S.svdq_layernorm_backward(dy, x, w, mean, rstd)
+    x.mul_(1.5)
+    dy.add_(0.25)
+    graph.replay()
+    _, m2, r2 = S.svdq_layernorm(x, w, b)
+    for a, c in zip(out, S.svdq_layernorm_backward(dy, x, w, m2, r2)):
+        assert torch.equal(a, c)

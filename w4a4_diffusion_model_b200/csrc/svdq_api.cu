@@ -5,20 +5,26 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
+#include <type_traits>
 
 #include "svdq.h"
 #include "svdq_deltaquant.cuh"
 #include "svdq_gemm.cuh"
 #include "svdq_gemm_pair.cuh"
 #include "svdq_int4.cuh"
+#include "svdq_int8.cuh"
+#include "svdq_norm.cuh"
 #include "svdq_prepare.cuh"
 #include "svdq_quant.cuh"
 #include "svdq_quant_tma.cuh"
+#include "svdq_rope.cuh"
 #include "svdq_svd.cuh"
 
 // Device scratch of svdq_prepare_weights_static: the SVD workspace for callers
@@ -1143,3 +1149,5 @@ svdq_status svdq_check(void* stream) {
 }
 
 }  // extern "C"
+
+#include "svdq_block_api.cuh"

@@ -1,0 +1,468 @@
+// Host side of the operators around the 4-bit linear layer: the W8A8 linear
+// layer, layer norm (forward, backward, with the 8-bit quantizer) and rotary
+// positions. Part of the translation unit svdq_api.cu, whose error, device and
+// tensor-map helpers it uses.
+#pragma once
+
+namespace {
+
+cudaLaunchConfig_t pdl_config(dim3 grid, dim3 block, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+bool float_type(int t) { return t == SVDQ_BF16 || t == SVDQ_FP16 || t == SVDQ_FP32; }
+int type_bytes(int t) { return t == SVDQ_FP32 ? 4 : 2; }
+
+svdq_status check_pointers(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return fail(SVDQ_ERR_MISALIGNED, "every pointer must be 16-byte aligned");
+  return SVDQ_OK;
+}
+
+// A matrix of `rows` rows of `cols` values with row stride ld: rows must not
+// overlap, and offsets must stay within 2^62 bytes.
+svdq_status check_rows(const char* what, int64_t rows, int64_t cols, int64_t ld) {
+  if (rows > 1 && (ld < cols || ld > (1ll << 40)))
+    return fail(SVDQ_ERR_INVALID_ARG, "%s: row stride %lld for rows of %lld", what, (long long)ld, (long long)cols);
+  return SVDQ_OK;
+}
+
+template <typename T>
+struct Tag {
+  using type = T;
+};
+
+template <typename F>
+svdq_status with_type(int dtype, F&& f) {
+  switch (dtype) {
+    case SVDQ_BF16: return f(Tag<__nv_bfloat16>());
+    case SVDQ_FP16: return f(Tag<__half>());
+    default: return f(Tag<float>());
+  }
+}
+
+// ---------------------------------------------------------------- 8-bit quantizer
+constexpr int64_t kInt8MaxK = 131072;   // 127^2 K < 2^31
+
+svdq_status check_int8_k(int64_t rows, int64_t K) {
+  if (rows < 0 || rows > (1ll << 31) - 1 || K < 16 || K % 16 || K > kInt8MaxK)
+    return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "int8 matrix of %lld x K=%lld: need K a multiple of 16, 16 <= K <= %lld",
+                (long long)rows, (long long)K, (long long)kInt8MaxK);
+  return SVDQ_OK;
+}
+
+template <typename T, int NV, int MAXT>
+svdq_status launch_int8_quantize(const svdq::Int8QuantArgs& a, dim3 grid, dim3 block, cudaStream_t st) {
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pdl_config(grid, block, 0, st, attr);
+  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::int8_quantize_kernel<T, NV, MAXT>, a));
+  return SVDQ_OK;
+}
+
+int round_up(int v, int m) { return (v + m - 1) / m * m; }
+
+svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_t ldx, const float* mult, void* Q,
+                          float* S, void* stream) {
+  g_last_error[0] = 0;
+  svdq_status r = check_int8_k(M, K);
+  if (r != SVDQ_OK) return r;
+  if (!float_type(dtype)) return fail(SVDQ_ERR_INVALID_ARG, "unknown type %d", dtype);
+  if (M > 0 && (!X || !Q || !S)) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if ((r = check_pointers({X, mult, Q, S})) != SVDQ_OK) return r;
+  if ((r = check_rows("X", M, K, ldx)) != SVDQ_OK) return r;
+  if (M > 1 && ldx * type_bytes(dtype) % 16)
+    return fail(SVDQ_ERR_MISALIGNED, "row stride %lld is not a multiple of 16 bytes", (long long)ldx);
+  if ((r = check_device()) != SVDQ_OK) return r;
+  if (M == 0) return SVDQ_OK;
+  const svdq::Int8QuantArgs a{X, ldx, mult, static_cast<int8_t*>(Q), S, M, (int)K};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return with_type(dtype, [&](auto tag) -> svdq_status {
+    using T = typename decltype(tag)::type;
+    const int vecs = (int)K / svdq::kVecN<T>;
+    const int64_t sms = sm_count();
+    if (vecs <= 128) {   // rows a warp holds: eight of them per block
+      const unsigned grid = (unsigned)std::min<int64_t>((M + 7) / 8, sms * 8);
+      const dim3 block(32, 8);
+      if (vecs <= 32) return launch_int8_quantize<T, 1, 256>(a, grid, block, st);
+      if (vecs <= 64) return launch_int8_quantize<T, 2, 256>(a, grid, block, st);
+      return launch_int8_quantize<T, 4, 256>(a, grid, block, st);
+    }
+    const unsigned grid = (unsigned)std::min<int64_t>(M, sms * 8);
+    if (vecs <= 512) return launch_int8_quantize<T, 2, 256>(a, grid, round_up((vecs + 1) / 2, 32), st);
+    if (vecs <= 1024) return launch_int8_quantize<T, 4, 256>(a, grid, round_up((vecs + 3) / 4, 32), st);
+    if (vecs <= 4096) return launch_int8_quantize<T, 4, 1024>(a, grid, round_up((vecs + 3) / 4, 32), st);
+    return launch_int8_quantize<T, 0, 1024>(a, grid, 1024, st);
+  });
+}
+
+// ---------------------------------------------------------------- W8A8 product
+template <int NB, typename OT>
+svdq_status launch_int8_gemm(const svdq::Int8GemmArgs& args, const void* Qx, const void* Qw, int splits,
+                             cudaStream_t st) {
+  using C = svdq::Int8Cfg<NB>;
+  auto kern = svdq::svdq_int8_gemm_kernel<NB, OT>;
+  static std::atomic<int> done[kMaxDevices];
+  cudaError_t err = cudaSuccess;
+  per_device_once(done, current_device(), [&err, kern] {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+    return err == cudaSuccess ? 1 : 0;
+  });
+  if (err != cudaSuccess)
+    return fail(SVDQ_ERR_CUDA, "cudaFuncSetAttribute(svdq_int8_gemm_kernel): %s", cudaGetErrorString(err));
+  svdq::Int8GemmArgs a = args;
+  a.a_rows = a.M >= 128 ? 128 : round_up(a.M, 8);
+  CUtensorMap tx, tw;
+  svdq_status r;
+  if ((r = make_tmap(&tx, Qx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.M, svdq::kI8KTile,
+                     (uint32_t)a.a_rows, CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
+    return r;
+  if ((r = make_tmap(&tw, Qw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N, svdq::kI8KTile, NB,
+                     CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
+    return r;
+  const int64_t tiles = (int64_t)((a.N + NB - 1) / NB) * ((a.M + 127) / 128);
+  if (tiles > (1ll << 31) - 1) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "too many tiles");
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg =
+      pdl_config(dim3((unsigned)tiles, 1, (unsigned)splits), svdq::kI8Threads, C::kBytes, st, attr);
+  if (splits > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = splits;
+    cfg.numAttrs = 2;
+  }
+  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, tx, tw, a));
+  return SVDQ_OK;
+}
+
+// ---------------------------------------------------------------- norm
+constexpr int64_t kNormMaxC = 16384;
+
+struct NormCall {
+  int64_t M, C;
+  int dtype, w_dtype;
+  int64_t rows_per_group;
+  unsigned flags;
+};
+
+svdq_status check_norm(const NormCall& n) {
+  if (n.M < 0 || n.M > (1ll << 31) - 1 || n.C < 1 || n.C > kNormMaxC)
+    return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "norm of %lld rows of %lld: need 1 <= C <= %lld", (long long)n.M,
+                (long long)n.C, (long long)kNormMaxC);
+  if (!float_type(n.dtype)) return fail(SVDQ_ERR_INVALID_ARG, "unknown type %d", n.dtype);
+  if (n.w_dtype != n.dtype && n.w_dtype != SVDQ_FP32)
+    return fail(SVDQ_ERR_INVALID_ARG, "weight and bias have the type of X or fp32");
+  if (n.rows_per_group < 0) return fail(SVDQ_ERR_INVALID_ARG, "rows_per_group %lld", (long long)n.rows_per_group);
+  if (n.flags & ~(unsigned)SVDQ_NORM_ADD_ONE) return fail(SVDQ_ERR_INVALID_ARG, "unknown flags 0x%x", n.flags);
+  return SVDQ_OK;
+}
+
+int64_t norm_group_rows(const NormCall& n) {
+  return n.rows_per_group == 0 || n.rows_per_group > n.M ? std::max<int64_t>(n.M, 1) : n.rows_per_group;
+}
+int64_t norm_groups(const NormCall& n) {
+  const int64_t rows = norm_group_rows(n);
+  return std::max<int64_t>(1, (n.M + rows - 1) / rows);
+}
+
+// Calls f<T, WT, VEC>: 16-byte pieces when the rows, their strides and C allow it.
+template <typename F>
+svdq_status norm_dispatch(const NormCall& n, std::initializer_list<int64_t> strides, F&& f) {
+  return with_type(n.dtype, [&](auto tag) -> svdq_status {
+    using T = typename decltype(tag)::type;
+    bool vec = n.C % svdq::kVecN<T> == 0;
+    if (n.M > 1)
+      for (int64_t ld : strides) vec = vec && ld % svdq::kVecN<T> == 0;
+    auto go = [&](auto wtag) -> svdq_status {
+      if (vec) return f(tag, wtag, std::true_type());
+      return f(tag, wtag, std::false_type());
+    };
+    if (n.w_dtype == n.dtype) return go(tag);
+    return go(Tag<float>());
+  });
+}
+
+// Threads per row and pieces per thread: f gets NV and the block's limit.
+// Pieces: 16-byte vectors, at most 4096 of them, or single values.
+template <bool VEC, typename F>
+svdq_status norm_width(int pieces, F&& f) {
+  if constexpr (VEC) {
+    if (pieces <= 256) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 512>());
+    if (pieces <= 1024) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 512>());
+    if (pieces <= 2048) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 1024>());
+    return f(std::integral_constant<int, 4>(), std::integral_constant<int, 1024>());
+  } else {
+    if (pieces <= 2048) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 512>());
+    return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1024>());
+  }
+}
+
+template <bool QUANT>
+svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStream_t st) {
+  return norm_dispatch(n, {a.ldx, QUANT ? (int64_t)0 : (int64_t)a.ldy}, [&](auto tag, auto wtag, auto vec) -> svdq_status {
+    using T = typename decltype(tag)::type;
+    using WT = typename decltype(wtag)::type;
+    constexpr bool VEC = decltype(vec)::value;
+    const int pieces = (int)n.C / (VEC ? svdq::kVecN<T> : 1);
+    return norm_width<VEC>(pieces, [&](auto nv, auto maxt) -> svdq_status {
+      constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
+      const int threads = round_up((pieces + NV - 1) / NV, 32);
+      const dim3 block(threads, threads == 32 ? 8 : 1);
+      const unsigned grid = (unsigned)std::min<int64_t>((n.M + block.y - 1) / block.y, (int64_t)sm_count() * 16);
+      cudaLaunchAttribute attr[1];
+      cudaLaunchConfig_t cfg = pdl_config(grid, block, 0, st, attr);
+      SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::layernorm_kernel<T, WT, NV, MAXT, VEC, QUANT>, a));
+      return SVDQ_OK;
+    });
+  });
+}
+
+// Row chunks per group of the backward pass: about two blocks per SM over all
+// groups. More groups than that: each block takes a group's rows alone, and no
+// partial sums are kept.
+int64_t norm_chunks(const NormCall& n) {
+  const int64_t groups = norm_groups(n);
+  const int64_t per = std::max<int64_t>(1, 2ll * sm_count() / groups);
+  return std::min<int64_t>(per, std::max<int64_t>(1, (norm_group_rows(n) + 3) / 4));
+}
+
+size_t norm_workspace_bytes(const NormCall& n) {
+  const int64_t chunks = norm_chunks(n);
+  return chunks == 1 ? 0 : (size_t)(2 * chunks * norm_groups(n) * n.C) * 4u;
+}
+
+// ---------------------------------------------------------------- rotary positions
+template <typename T>
+svdq_status launch_rope(svdq::RopeArgs a, bool halves, cudaStream_t st) {
+  constexpr int V = svdq::kVecN<T>;
+  bool vec = (a.D - a.R) % V == 0 && (halves ? a.R / 2 : a.R) % V == 0 && a.D % V == 0;
+  if (a.T > 1) vec = vec && a.xt % V == 0 && a.yt % V == 0;
+  if (a.heads > 1) vec = vec && a.xh % V == 0 && a.yh % V == 0;
+  // few tokens: several blocks share a token's heads
+  const int64_t want = 4ll * sm_count();
+  const int shares = (int)std::min<int64_t>(std::min<int64_t>(a.heads, 65535), std::max<int64_t>(1, want / a.T));
+  a.heads_per_block = (a.heads + shares - 1) / shares;
+  const dim3 grid((unsigned)std::min<int64_t>(a.T, 1ll << 30), (unsigned)((a.heads + a.heads_per_block - 1) / a.heads_per_block));
+  const int items = a.heads_per_block * (a.D / (vec ? (halves ? 2 * V : V) : 2));
+  const int threads = std::min(256, round_up(items, 32));
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pdl_config(grid, threads, 0, st, attr);
+  if (halves) {
+    if (vec) SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::rope_kernel<T, true, true>, a));
+    else SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::rope_kernel<T, true, false>, a));
+  } else {
+    if (vec) SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::rope_kernel<T, false, true>, a));
+    else SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::rope_kernel<T, false, false>, a));
+  }
+  return SVDQ_OK;
+}
+
+// Whether [T][heads][D] with these strides holds every element once.
+bool disjoint(int64_t T, int64_t heads, int64_t D, int64_t st, int64_t sh) {
+  if (T <= 1) return heads <= 1 || sh >= D;
+  if (heads <= 1) return st >= D;
+  return (sh >= D && st >= (heads - 1) * sh + D) || (st >= D && sh >= (T - 1) * st + D);
+}
+
+}  // namespace
+
+extern "C" {
+
+svdq_status svdq_int8_quantize_act(int64_t M, int64_t K, int x_dtype, const void* X, int64_t ldx,
+                                   const float* inv_lambda, void* Qx, float* Sx, void* stream) {
+  return int8_quantize(M, K, x_dtype, X, ldx, inv_lambda, Qx, Sx, stream);
+}
+
+svdq_status svdq_int8_quantize_weight(int64_t N, int64_t K, int w_dtype, const void* W_lin, int64_t ldw,
+                                      const float* lambda, void* Qw, float* Sw, void* stream) {
+  return int8_quantize(N, K, w_dtype, W_lin, ldw, lambda, Qw, Sw, stream);
+}
+
+svdq_status svdq_int8_linear(int64_t M, int64_t K, int64_t N, const void* Qx, const float* Sx, const void* Qw,
+                             const float* Sw, const float* bias, int y_dtype, void* Y, int64_t ldy, void* stream) {
+  g_last_error[0] = 0;
+  svdq_status r = check_int8_k(M, K);
+  if (r != SVDQ_OK) return r;
+  if (N < 1 || N > (1ll << 24)) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "int8 linear with N=%lld", (long long)N);
+  if (!float_type(y_dtype)) return fail(SVDQ_ERR_INVALID_ARG, "unknown type %d", y_dtype);
+  if (!Qw || !Sw || (M > 0 && (!Qx || !Sx || !Y))) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if ((r = check_pointers({Qx, Sx, Qw, Sw, bias, Y})) != SVDQ_OK) return r;
+  if ((r = check_rows("Y", M, N, ldy)) != SVDQ_OK) return r;
+  if ((r = check_device()) != SVDQ_OK) return r;
+  if (M == 0) return SVDQ_OK;
+  const svdq::Int8GemmArgs a{Sx, Sw, bias, Y, ldy, (int)M, (int)N, (int)K, 0};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return with_type(y_dtype, [&](auto tag) -> svdq_status {
+    using T = typename decltype(tag)::type;
+    return launch_int8_gemm<128, T>(a, Qx, Qw, 1, st);
+  });
+}
+
+svdq_status svdq_layernorm(int64_t M, int64_t C, int dtype, int w_dtype, const void* X, int64_t ldx,
+                           const void* weight, const void* bias, int64_t rows_per_group, float eps,
+                           unsigned int flags, void* Y, int64_t ldy, float* mean, float* rstd, void* stream) {
+  g_last_error[0] = 0;
+  const NormCall n{M, C, dtype, w_dtype, rows_per_group, flags};
+  svdq_status r = check_norm(n);
+  if (r != SVDQ_OK) return r;
+  if (!(eps >= 0.f)) return fail(SVDQ_ERR_INVALID_ARG, "eps must be >= 0");
+  if (M > 0 && (!X || !Y)) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if ((r = check_pointers({X, weight, bias, Y, mean, rstd})) != SVDQ_OK) return r;
+  if ((r = check_rows("X", M, C, ldx)) != SVDQ_OK || (r = check_rows("Y", M, C, ldy)) != SVDQ_OK) return r;
+  if ((r = check_device()) != SVDQ_OK) return r;
+  if (M == 0) return SVDQ_OK;
+  svdq::NormArgs a = {};
+  a.x = X; a.ldx = ldx; a.w = weight; a.b = bias; a.mean = mean; a.rstd = rstd;
+  a.M = M; a.rows_per_group = norm_group_rows(n); a.C = (int)C; a.eps = eps;
+  a.add = flags & SVDQ_NORM_ADD_ONE ? 1.f : 0.f;
+  a.y = Y; a.ldy = ldy;
+  return launch_layernorm<false>(n, a, static_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_int8_layernorm_quantize(int64_t M, int64_t C, int dtype, int w_dtype, const void* X, int64_t ldx,
+                                         const void* weight, const void* bias, int64_t rows_per_group, float eps,
+                                         unsigned int flags, const float* inv_lambda, void* Qx, float* Sx,
+                                         void* stream) {
+  g_last_error[0] = 0;
+  const NormCall n{M, C, dtype, w_dtype, rows_per_group, flags};
+  svdq_status r = check_norm(n);
+  if (r != SVDQ_OK) return r;
+  if (C % 16) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "C=%lld must be a multiple of 16", (long long)C);
+  if (!(eps >= 0.f)) return fail(SVDQ_ERR_INVALID_ARG, "eps must be >= 0");
+  if (M > 0 && (!X || !Qx || !Sx)) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if ((r = check_pointers({X, weight, bias, inv_lambda, Qx, Sx})) != SVDQ_OK) return r;
+  if ((r = check_rows("X", M, C, ldx)) != SVDQ_OK) return r;
+  if ((r = check_device()) != SVDQ_OK) return r;
+  if (M == 0) return SVDQ_OK;
+  svdq::NormArgs a = {};
+  a.x = X; a.ldx = ldx; a.w = weight; a.b = bias;
+  a.M = M; a.rows_per_group = norm_group_rows(n); a.C = (int)C; a.eps = eps;
+  a.add = flags & SVDQ_NORM_ADD_ONE ? 1.f : 0.f;
+  a.inv_lambda = inv_lambda; a.q = static_cast<int8_t*>(Qx); a.s = Sx;
+  return launch_layernorm<true>(n, a, static_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_layernorm_backward_workspace(int64_t M, int64_t C, int64_t rows_per_group, size_t* bytes) {
+  g_last_error[0] = 0;
+  const NormCall n{M, C, SVDQ_FP32, SVDQ_FP32, rows_per_group, 0};
+  svdq_status r = check_norm(n);
+  if (r != SVDQ_OK) return r;
+  if (!bytes) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  *bytes = norm_workspace_bytes(n);
+  return SVDQ_OK;
+}
+
+svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype, const void* dY, int64_t lddy,
+                                    const void* X, int64_t ldx, const void* weight, const float* mean,
+                                    const float* rstd, int64_t rows_per_group, unsigned int flags, void* dX,
+                                    int64_t lddx, float* dweight, float* dbias, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  g_last_error[0] = 0;
+  const NormCall n{M, C, dtype, w_dtype, rows_per_group, flags};
+  svdq_status r = check_norm(n);
+  if (r != SVDQ_OK) return r;
+  if (M > 0 && (!dY || !X || !mean || !rstd || !dX)) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  if ((r = check_pointers({dY, X, weight, mean, rstd, dX, dweight, dbias, workspace})) != SVDQ_OK) return r;
+  if ((r = check_rows("dY", M, C, lddy)) != SVDQ_OK || (r = check_rows("X", M, C, ldx)) != SVDQ_OK ||
+      (r = check_rows("dX", M, C, lddx)) != SVDQ_OK)
+    return r;
+  const bool sums = dweight || dbias;
+  const size_t need = sums ? norm_workspace_bytes(n) : 0;
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(SVDQ_ERR_BUFFER_TOO_SMALL, "workspace of %zu bytes, need %zu", workspace ? workspace_bytes : 0, need);
+  if ((r = check_device()) != SVDQ_OK) return r;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0) {   // the sums over no rows
+    if (dweight) SVDQ_CUDA(cudaMemsetAsync(dweight, 0, (size_t)C * 4, st));
+    if (dbias) SVDQ_CUDA(cudaMemsetAsync(dbias, 0, (size_t)C * 4, st));
+    return SVDQ_OK;
+  }
+  svdq::NormArgs a = {};
+  a.x = X; a.ldx = ldx; a.w = weight; a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
+  a.M = M; a.rows_per_group = norm_group_rows(n); a.C = (int)C;
+  a.add = flags & SVDQ_NORM_ADD_ONE ? 1.f : 0.f;
+  a.dy = dY; a.lddy = lddy; a.dx = dX; a.lddx = lddx; a.dw = dweight; a.db = dbias;
+  a.chunks = (int)norm_chunks(n);
+  a.part = need ? static_cast<float*>(workspace) : nullptr;
+  const int64_t groups = norm_groups(n);
+  r = norm_dispatch(n, {lddy, ldx, lddx}, [&](auto tag, auto wtag, auto vec) -> svdq_status {
+    using T = typename decltype(tag)::type;
+    using WT = typename decltype(wtag)::type;
+    constexpr bool VEC = decltype(vec)::value;
+    const int pieces = (int)n.C / (VEC ? svdq::kVecN<T> : 1);
+    return norm_width<VEC>(pieces, [&](auto nv, auto maxt) -> svdq_status {
+      constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
+      constexpr int N = VEC ? svdq::kVecN<T> : 1;
+      const int threads = round_up((pieces + NV - 1) / NV, 32);
+      const dim3 block(threads, std::max(1, std::min(512 / threads, 8)));
+      const size_t smem = block.y > 1 ? (size_t)NV * N * threads * 4 : 0;
+      cudaLaunchAttribute attr[1];
+      cudaLaunchConfig_t cfg = pdl_config((unsigned)(groups * a.chunks), block, smem, st, attr);
+      SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::layernorm_backward_kernel<T, WT, NV, MAXT, VEC>, a));
+      return SVDQ_OK;
+    });
+  });
+  if (r != SVDQ_OK || !a.part) return r;
+  const int64_t cols = groups * C;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((cols + 31) / 32), 2), 256, 0, st, attr);
+  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::layernorm_partials_kernel, static_cast<const float*>(a.part), dweight,
+                               dbias, (long long)cols, a.chunks));
+  return SVDQ_OK;
+}
+
+svdq_status svdq_rope(int64_t T, int32_t heads, int32_t D, int dtype, const void* X, int64_t x_token_stride,
+                      int64_t x_head_stride, void* Y, int64_t y_token_stride, int64_t y_head_stride,
+                      const void* positions, int pos_dtype, int64_t pos_rows, int32_t axes, const int32_t* axis_dims,
+                      const double* freqs, unsigned int flags, void* stream) {
+  g_last_error[0] = 0;
+  if (T < 0 || T > (1ll << 31) - 1 || heads < 0 || heads > 65535 || D < 2 || D > svdq::kRopeMaxD || D % 2)
+    return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "rope T=%lld heads=%d D=%d: need an even D in [2, %d]", (long long)T,
+                (int)heads, (int)D, svdq::kRopeMaxD);
+  if (!float_type(dtype)) return fail(SVDQ_ERR_INVALID_ARG, "unknown type %d", dtype);
+  if (pos_dtype != SVDQ_INT32 && pos_dtype != SVDQ_FP32) return fail(SVDQ_ERR_INVALID_ARG, "positions are int32 or fp32");
+  if (flags & ~(unsigned)(SVDQ_ROPE_HALVES | SVDQ_ROPE_INVERSE)) return fail(SVDQ_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+  if (axes < 1 || axes > svdq::kRopeMaxAxes || !axis_dims)
+    return fail(SVDQ_ERR_INVALID_ARG, "axes=%d: need 1 to %d of them", (int)axes, svdq::kRopeMaxAxes);
+  svdq::RopeArgs a = {};
+  int64_t R = 0;
+  for (int i = 0; i < axes; ++i) {
+    if (axis_dims[i] < 2 || axis_dims[i] % 2 || axis_dims[i] > D)
+      return fail(SVDQ_ERR_INVALID_ARG, "axis %d has %d elements: need an even number of at least 2", i, (int)axis_dims[i]);
+    R += axis_dims[i];
+    a.axis_end[i] = (int)(R / 2);
+  }
+  if (R > D) return fail(SVDQ_ERR_INVALID_ARG, "the axes have %lld elements, a head has %d", (long long)R, (int)D);
+  const bool any = T > 0 && heads > 0;
+  if (any && (!X || !Y || !positions || !freqs)) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
+  svdq_status r;
+  if ((r = check_pointers({X, Y, positions, freqs})) != SVDQ_OK) return r;
+  if (any && (pos_rows < 1 || T % pos_rows))
+    return fail(SVDQ_ERR_INVALID_ARG, "%lld tokens with %lld rows of positions", (long long)T, (long long)pos_rows);
+  for (int64_t s : {x_token_stride, x_head_stride, y_token_stride, y_head_stride})
+    if (any && (s < 0 || s > (1ll << 40))) return fail(SVDQ_ERR_INVALID_ARG, "stride %lld", (long long)s);
+  if (any && !disjoint(T, heads, D, y_token_stride, y_head_stride))
+    return fail(SVDQ_ERR_INVALID_ARG, "the heads of Y overlap");
+  if (any && X == Y && ((T > 1 && x_token_stride != y_token_stride) || (heads > 1 && x_head_stride != y_head_stride)))
+    return fail(SVDQ_ERR_INVALID_ARG, "in place, X and Y have the same strides");
+  if ((r = check_device()) != SVDQ_OK) return r;
+  if (!any) return SVDQ_OK;
+  a.x = X; a.y = Y; a.xt = x_token_stride; a.xh = x_head_stride; a.yt = y_token_stride; a.yh = y_head_stride;
+  a.pos = positions; a.freq = freqs; a.T = T; a.pos_rows = pos_rows; a.heads = heads; a.D = D; a.R = (int)R;
+  a.axes = axes; a.pos_fp32 = pos_dtype == SVDQ_FP32; a.inverse = (flags & SVDQ_ROPE_INVERSE) != 0;
+  return with_type(dtype, [&](auto tag) -> svdq_status {
+    using E = typename decltype(tag)::type;
+    return launch_rope<E>(a, (flags & SVDQ_ROPE_HALVES) != 0, static_cast<cudaStream_t>(stream));
+  });
+}
+
+}  // extern "C"

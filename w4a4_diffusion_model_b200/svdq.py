@@ -20,6 +20,12 @@ SVDQ_FUSED = 0
 SVDQ_UNFUSED = 1
 SVDQ_PREPARE_GIVEN_FACTORS = 1
 SVDQ_NEXT_FUSE_LOWRANK = 1
+SVDQ_NORM_ADD_ONE = 1
+SVDQ_ROPE_HALVES = 1
+SVDQ_ROPE_INVERSE = 2
+
+# svdq_dtype
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.int32: 3}
 
 STATUS = {
     0: "SVDQ_OK", 1: "SVDQ_ERR_INVALID_ARG", 2: "SVDQ_ERR_UNSUPPORTED_SHAPE", 3: "SVDQ_ERR_MISALIGNED",
@@ -35,6 +41,8 @@ EXPORTS = [
     "svdq_selftest_timeout", "svdq_scales_to_canonical", "svdq_check",
     "svdq_int4_act_sizes", "svdq_int4_weight_sizes", "svdq_int4_quantize_residual", "svdq_int4_quantize_act",
     "svdq_int4_linear", "svdq_deltaquant_sizes", "svdq_deltaquant_encode",
+    "svdq_int8_quantize_act", "svdq_int8_quantize_weight", "svdq_int8_linear", "svdq_layernorm",
+    "svdq_int8_layernorm_quantize", "svdq_layernorm_backward_workspace", "svdq_layernorm_backward", "svdq_rope",
 ]
 
 
@@ -99,6 +107,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.svdq_deltaquant_sizes.restype = st
     lib.svdq_deltaquant_encode.argtypes = [i64, i64, i64, i64, vp, vp, vp, vp, vp]
     lib.svdq_deltaquant_encode.restype = st
+    i32, u32, f32 = ctypes.c_int32, ctypes.c_uint, ctypes.c_float
+    for name in ("svdq_int8_quantize_act", "svdq_int8_quantize_weight"):
+        getattr(lib, name).argtypes, getattr(lib, name).restype = [i64, i64, st, vp, i64, vp, vp, vp, vp], st
+    lib.svdq_int8_linear.argtypes = [i64, i64, i64, vp, vp, vp, vp, vp, st, vp, i64, vp]
+    lib.svdq_int8_linear.restype = st
+    lib.svdq_layernorm.argtypes = [i64, i64, st, st, vp, i64, vp, vp, i64, f32, u32, vp, i64, vp, vp, vp]
+    lib.svdq_layernorm.restype = st
+    lib.svdq_int8_layernorm_quantize.argtypes = [i64, i64, st, st, vp, i64, vp, vp, i64, f32, u32, vp, vp, vp, vp]
+    lib.svdq_int8_layernorm_quantize.restype = st
+    lib.svdq_layernorm_backward_workspace.argtypes = [i64, i64, i64, P(sz)]
+    lib.svdq_layernorm_backward_workspace.restype = st
+    lib.svdq_layernorm_backward.argtypes = [i64, i64, st, st, vp, i64, vp, i64, vp, vp, vp, i64, u32, vp, i64, vp, vp,
+                                            vp, sz, vp]
+    lib.svdq_layernorm_backward.restype = st
+    lib.svdq_rope.argtypes = [i64, i32, i32, st, vp, i64, i64, vp, i64, i64, vp, st, i64, i32, P(i32), vp, u32, vp]
+    lib.svdq_rope.restype = st
     _lib = lib
     return lib
 
@@ -355,6 +379,295 @@ def svdq_deltaquant_encode(X: torch.Tensor, dims: tuple[int, int, int], out: tup
         core, Qd, Sd = out
     _check(load().svdq_deltaquant_encode(F, H, W, C, _ptr(X), _ptr(core), _ptr(Qd), _ptr(Sd), _stream()))
     return core, Qd, Sd
+
+
+# ---------------------------------------------------------------- around the 4-bit linear layer
+# W8A8 linear, layer norm and rotary positions. Rows may have a stride; every
+# tensor of a call lives on one CUDA device, which need not be the current one.
+
+def _float_type(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise ValueError(f"{what} must be bf16, fp16 or fp32, not {t.dtype}")
+    return DTYPES[t.dtype]
+
+
+def _device(X: torch.Tensor, *others: torch.Tensor | None) -> torch.device:
+    dev = X.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on a CUDA device")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: all must live on one device")
+    return dev
+
+
+def _rows(t: torch.Tensor, what: str) -> tuple[int, int]:
+    """(address, row stride) of a matrix whose rows are contiguous."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{what} must be a matrix with contiguous rows")
+    return t.data_ptr(), t.stride(0)
+
+
+def _dense(t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, what: str) -> int | None:
+    """Address of a contiguous tensor of this shape and type (None: no tensor)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _call(dev: torch.device, fn, *args) -> None:
+    """fn(*args, stream) on dev's current stream, with dev current."""
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if status:
+        _check(status)
+
+
+@dataclass
+class Int8Weights:
+    """A W8A8 layer: codes and scales of lambda * W_lin per output channel, and
+    what its calls multiply and add."""
+    N: int
+    K: int
+    Qw: torch.Tensor                    # int8 [N][K]
+    Sw: torch.Tensor                    # fp32 [N]
+    inv_lam: torch.Tensor | None = None  # fp32 [K]: the activation's smoothing factors
+    bias: torch.Tensor | None = None    # fp32 [N]
+
+
+def svdq_int8_prepare_weights(W_lin: torch.Tensor, lam: torch.Tensor | None = None,
+                              inv_lam: torch.Tensor | None = None, bias: torch.Tensor | None = None) -> Int8Weights:
+    """8-bit codes of W_lin [N][K] (bf16, fp16 or fp32), one scale per output channel. lam and
+    inv_lam fp32 [K]: smoothing factors, as svdq_prepare_weights returns them (both or neither)."""
+    if (lam is None) != (inv_lam is None):
+        raise ValueError("lam and inv_lam come together")
+    dev = _device(W_lin, lam, inv_lam, bias)
+    wt = _float_type(W_lin, "W_lin")
+    wp, ldw = _rows(W_lin, "W_lin")
+    N, K = W_lin.shape
+    lp = _dense(lam, (K,), torch.float32, "lam")
+    _dense(inv_lam, (K,), torch.float32, "inv_lam")
+    if bias is not None:
+        if bias.shape != (N,):
+            raise ValueError(f"bias must have {N} values")
+        bias = bias.float().contiguous()
+    Qw = torch.empty(N, K, dtype=torch.int8, device=dev)
+    Sw = torch.empty(N, dtype=torch.float32, device=dev)
+    _call(dev, load().svdq_int8_quantize_weight, N, K, wt, wp, ldw, lp, Qw.data_ptr(), Sw.data_ptr())
+    return Int8Weights(N, K, Qw, Sw, inv_lam, bias)
+
+
+def svdq_int8_quantize_act(X: torch.Tensor, inv_lambda: torch.Tensor | None = None, out: tuple | None = None):
+    """8-bit codes of X [M][K] (bf16, fp16 or fp32; rows may be strided), one scale per token.
+    Returns (Qx int8 [M][K], Sx fp32 [M])."""
+    dev = _device(X, inv_lambda)
+    xt = _float_type(X, "X")
+    xp, ldx = _rows(X, "X")
+    M, K = X.shape
+    lp = _dense(inv_lambda, (K,), torch.float32, "inv_lambda")
+    if out is None:
+        Qx = torch.empty(M, K, dtype=torch.int8, device=dev)
+        Sx = torch.empty(M, dtype=torch.float32, device=dev)
+        qp, sp = Qx.data_ptr(), Sx.data_ptr()
+    else:
+        Qx, Sx = out
+        _device(X, Qx, Sx)
+        qp, sp = _dense(Qx, (M, K), torch.int8, "Qx"), _dense(Sx, (M,), torch.float32, "Sx")
+    _call(dev, load().svdq_int8_quantize_act, M, K, xt, xp, ldx, lp, qp, sp)
+    return Qx, Sx
+
+
+def svdq_int8_linear(Qx: torch.Tensor, Sx: torch.Tensor, W: Int8Weights, dtype: torch.dtype = torch.bfloat16,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """Y [M][N] = Sx Sw (Qx Qw^T) + bias of a W8A8 layer, in dtype (or out's: rows may be strided)."""
+    dev = _device(Qx, Sx, W.Qw, W.Sw, W.bias, out)
+    M, K, N = Qx.shape[0], W.K, W.N
+    Y = torch.empty(M, N, dtype=dtype, device=dev) if out is None else out
+    if Y.shape != (M, N):
+        raise ValueError(f"out must be [{M}][{N}]")
+    yt = _float_type(Y, "out")
+    yp, ldy = _rows(Y, "out")
+    _call(dev, load().svdq_int8_linear, M, K, N, _dense(Qx, (M, K), torch.int8, "Qx"),
+          _dense(Sx, (M,), torch.float32, "Sx"), _dense(W.Qw, (N, K), torch.int8, "Qw"),
+          _dense(W.Sw, (N,), torch.float32, "Sw"), _dense(W.bias, (N,), torch.float32, "bias"), yt, yp, ldy)
+    return Y
+
+
+def _norm_params(X: torch.Tensor, weight: torch.Tensor | None, bias: torch.Tensor | None, rows_per_group: int | None):
+    """(w_dtype, weight address, bias address, rows per group, groups) of a norm over X. weight and bias are [C], or
+    [groups][C] for groups of rows_per_group rows (default: M / groups, which must be whole)."""
+    M, C = X.shape
+    first = weight if weight is not None else bias
+    if first is None:
+        if rows_per_group and rows_per_group < 0:
+            raise ValueError("rows_per_group must not be negative")
+        rows = rows_per_group or 0
+        groups = max(1, -(-M // rows)) if rows else 1
+        return DTYPES[X.dtype], None, None, rows, groups
+    if first.dtype != X.dtype and first.dtype != torch.float32:
+        raise ValueError(f"weight and bias must be {X.dtype} or torch.float32")
+    if first.dim() == 1:
+        if rows_per_group:
+            raise ValueError("weight and bias of row groups are [groups][C]")
+        shape, rows, groups = (C,), 0, 1
+    else:
+        groups = first.shape[0]
+        shape = (groups, C)
+        if rows_per_group is None:
+            if groups < 1 or M % groups:
+                raise ValueError(f"{M} rows do not divide into {groups} groups: give rows_per_group")
+            rows = M // groups
+        else:
+            rows = rows_per_group
+        if M and (rows < 0 or groups != (-(-M // rows) if rows else 1)):
+            raise ValueError(f"{M} rows in groups of {rows} do not have {groups} rows of weight and bias")
+    return (DTYPES[first.dtype], _dense(weight, shape, first.dtype, "weight"), _dense(bias, shape, first.dtype, "bias"),
+            rows, groups)
+
+
+def svdq_layernorm(X: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                   eps: float = 1e-6, rows_per_group: int | None = None, add_one: bool = False,
+                   out: torch.Tensor | None = None, stats: bool = True):
+    """Layer norm of X's rows [M][C] (bf16, fp16 or fp32). weight and bias: [C], or [groups][C] for a modulated norm
+    whose rows share them in groups of rows_per_group (default: M / groups); X's type or fp32. add_one: the weight is
+    1 + weight. Returns (Y, mean, rstd): mean and rstd fp32 [M] for the backward pass (None with stats=False)."""
+    dev = _device(X, weight, bias, out)
+    xt = _float_type(X, "X")
+    xp, ldx = _rows(X, "X")
+    M, C = X.shape
+    wt, wp, bp, rows, _ = _norm_params(X, weight, bias, rows_per_group)
+    if out is None:
+        out = torch.empty(M, C, dtype=X.dtype, device=dev)
+        yp, ldy = out.data_ptr(), C
+    else:
+        if out.shape != X.shape or out.dtype != X.dtype:
+            raise ValueError("out must have X's shape and type")
+        yp, ldy = _rows(out, "out")
+    mean = rstd = mp = rp = None
+    if stats:
+        mean = torch.empty(M, dtype=torch.float32, device=dev)
+        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    _call(dev, load().svdq_layernorm, M, C, xt, wt, xp, ldx, wp, bp, rows, eps, SVDQ_NORM_ADD_ONE if add_one else 0,
+          yp, ldy, mp, rp)
+    return out, mean, rstd
+
+
+def svdq_int8_layernorm_quantize(X: torch.Tensor, weight: torch.Tensor | None = None,
+                                 bias: torch.Tensor | None = None, inv_lambda: torch.Tensor | None = None,
+                                 eps: float = 1e-6, rows_per_group: int | None = None, add_one: bool = False,
+                                 out: tuple | None = None):
+    """svdq_layernorm straight to the 8-bit codes of the next product: (Qx int8 [M][C], Sx fp32 [M]). The norm is not
+    rounded to X's type before it is quantized."""
+    dev = _device(X, weight, bias, inv_lambda)
+    xt = _float_type(X, "X")
+    xp, ldx = _rows(X, "X")
+    M, C = X.shape
+    wt, wp, bp, rows, _ = _norm_params(X, weight, bias, rows_per_group)
+    lp = _dense(inv_lambda, (C,), torch.float32, "inv_lambda")
+    if out is None:
+        out = (torch.empty(M, C, dtype=torch.int8, device=dev), torch.empty(M, dtype=torch.float32, device=dev))
+    Qx, Sx = out
+    _device(X, Qx, Sx)
+    _call(dev, load().svdq_int8_layernorm_quantize, M, C, xt, wt, xp, ldx, wp, bp, rows, eps,
+          SVDQ_NORM_ADD_ONE if add_one else 0, lp, _dense(Qx, (M, C), torch.int8, "Qx"),
+          _dense(Sx, (M,), torch.float32, "Sx"))
+    return Qx, Sx
+
+
+def svdq_layernorm_backward_workspace(M: int, C: int, rows_per_group: int = 0) -> int:
+    v = ctypes.c_size_t()
+    _check(load().svdq_layernorm_backward_workspace(M, C, rows_per_group, ctypes.byref(v)))
+    return v.value
+
+
+def svdq_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
+                            rstd: torch.Tensor, rows_per_group: int | None = None, add_one: bool = False,
+                            out: torch.Tensor | None = None, params: bool = True):
+    """Gradients of svdq_layernorm: (dX in X's type, dweight, dbias). dweight and dbias are fp32, of weight's shape
+    ([C] without a weight), or None with params=False."""
+    dev = _device(X, dY, weight, mean, rstd, out)
+    xt = _float_type(X, "X")
+    xp, ldx = _rows(X, "X")
+    M, C = X.shape
+    if dY.shape != X.shape or dY.dtype != X.dtype:
+        raise ValueError("dY must have X's shape and type")
+    gp, ldg = _rows(dY, "dY")
+    wt, wp, _, rows, groups = _norm_params(X, weight, None, rows_per_group)
+    mp, rp = _dense(mean, (M,), torch.float32, "mean"), _dense(rstd, (M,), torch.float32, "rstd")
+    if out is None:
+        out = torch.empty(M, C, dtype=X.dtype, device=dev)
+        op, ldo = out.data_ptr(), C
+    else:
+        if out.shape != X.shape or out.dtype != X.dtype:
+            raise ValueError("out must have X's shape and type")
+        op, ldo = _rows(out, "out")
+    dw = db = dwp = dbp = work = kp = None
+    ws = 0
+    if params:
+        shape = weight.shape if weight is not None else (C,) if groups == 1 else (groups, C)
+        new = torch.empty if M else torch.zeros
+        dw = new(shape, dtype=torch.float32, device=dev)
+        db = new(shape, dtype=torch.float32, device=dev)
+        dwp, dbp = dw.data_ptr(), db.data_ptr()
+        with torch.cuda.device(dev):
+            ws = svdq_layernorm_backward_workspace(M, C, rows)
+        if ws:
+            work = torch.empty(ws, dtype=torch.uint8, device=dev)
+            kp = work.data_ptr()
+    _call(dev, load().svdq_layernorm_backward, M, C, xt, wt, gp, ldg, xp, ldx, wp, mp, rp, rows,
+          SVDQ_NORM_ADD_ONE if add_one else 0, op, ldo, dwp, dbp, kp, ws)
+    return out, dw, db
+
+
+class RopeTable:
+    """The rotary frequencies of a head, laid out once: axis_dims (the elements of a head that each axis turns) and
+    freqs fp64 [sum(axis_dims) / 2] on the device, pair by pair."""
+
+    def __init__(self, axis_dims, freqs: torch.Tensor):
+        self.axis_dims = tuple(int(d) for d in axis_dims)
+        self.freqs = freqs
+        if any(d < 2 or d % 2 for d in self.axis_dims):
+            raise ValueError("every axis needs an even number of elements, at least 2")
+        _dense(freqs, (sum(self.axis_dims) // 2,), torch.float64, "freqs")
+        self._dims = (ctypes.c_int32 * len(self.axis_dims))(*self.axis_dims)
+
+
+def svdq_rope_table(axis_dims, theta: float = 10000.0, device="cuda") -> RopeTable:
+    """Frequencies theta^(-2i/d) for pair i of an axis of d elements."""
+    freqs = [theta ** (-2.0 * i / d) for d in axis_dims for i in range(d // 2)]
+    return RopeTable(axis_dims, torch.tensor(freqs, dtype=torch.float64, device=device))
+
+
+def svdq_rope(X: torch.Tensor, positions: torch.Tensor, table: RopeTable, interleaved: bool = True,
+              inverse: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Turns the heads of X [T][heads][D] (bf16, fp16 or fp32; token and head strides are free, so X may be the query
+    and key heads inside a merged QKV activation) by their tokens' positions [P][axes] (int32 or fp32; T a multiple
+    of P). interleaved: pairs (2i, 2i+1), else (i, i + R/2). inverse: the gradient of the rotation. Returns out, or
+    a new contiguous tensor; out may be X."""
+    dev = _device(X, positions, table.freqs, out)
+    xt = _float_type(X, "X")
+    if X.dim() != 3 or X.stride(2) != 1:
+        raise ValueError("X must be [T][heads][D] with contiguous heads")
+    T, H, D = X.shape
+    axes = len(table.axis_dims)
+    if positions.dim() != 2 or positions.shape[1] != axes or not positions.is_contiguous() or \
+            positions.dtype not in (torch.int32, torch.float32):
+        raise ValueError(f"positions must be a contiguous int32 or fp32 [P][{axes}] tensor")
+    if out is None:
+        out = torch.empty(T, H, D, dtype=X.dtype, device=dev)
+    elif out.shape != X.shape or out.dtype != X.dtype or out.stride(2) != 1:
+        raise ValueError("out must have X's shape and type, and contiguous heads")
+    _call(dev, load().svdq_rope, T, H, D, xt, X.data_ptr(), X.stride(0), X.stride(1), out.data_ptr(), out.stride(0),
+          out.stride(1), positions.data_ptr(), DTYPES[positions.dtype], positions.shape[0], axes, table._dims,
+          table.freqs.data_ptr(), (0 if interleaved else SVDQ_ROPE_HALVES) | (SVDQ_ROPE_INVERSE if inverse else 0))
+    return out
 
 
 def svdq_selftest_timeout() -> None:
