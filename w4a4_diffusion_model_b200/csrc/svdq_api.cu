@@ -143,14 +143,16 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 2-D row-major tensor [rows][cols] of `elem_bytes`-sized elements, box of
-// box_cols x box_rows, zero fill out of bounds.
+// 2-D row-major tensor [rows][cols] of `elem_bytes`-sized elements (rows
+// `row_bytes` apart, 0: dense), box of box_cols x box_rows, zero fill out of
+// bounds.
 svdq_status make_tmap(CUtensorMap* tm, const void* base, CUtensorMapDataType dt, int elem_bytes, uint64_t cols,
-                      uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
+                      uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz,
+                      uint64_t row_bytes = 0) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(SVDQ_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * (uint64_t)elem_bytes};
+  const cuuint64_t strides[1] = {row_bytes ? row_bytes : cols * (uint64_t)elem_bytes};
   const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(tm, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,

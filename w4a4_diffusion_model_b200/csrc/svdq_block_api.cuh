@@ -144,6 +144,72 @@ svdq_status launch_int8_gemm(const svdq::Int8GemmArgs& args, const void* Qx, con
   return SVDQ_OK;
 }
 
+cudaLaunchConfig_t int8_pair_config(int clusters, cudaStream_t st, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = pdl_config(2 * clusters, svdq::kP8Threads, svdq::kP8Bytes, st, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Clusters of the pair kernel that fit on the device at once (0: none); also
+// sets the kernel's shared-memory attribute there.
+template <typename OT>
+int int8_pair_clusters() {
+  static std::atomic<int> cache[kMaxDevices];
+  return per_device_once(cache, current_device(), [] {
+    auto kern = svdq::svdq_int8_gemm_pair_kernel<OT>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, svdq::kP8Bytes) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = int8_pair_config(sm_count() / 2, nullptr, attr);
+    std::swap(attr[0], attr[1]);
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, (void*)kern, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    return n + 1;
+  }) - 1;
+}
+
+template <typename OT>
+svdq_status launch_int8_pair(const svdq::Int8GemmArgs& a, const void* Qx, const void* Qw, int clusters,
+                             cudaStream_t st) {
+  CUtensorMap tx, tw, ty;
+  svdq_status r;
+  if ((r = make_tmap(&tx, Qx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.M, svdq::kI8KTile, 128,
+                     CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
+    return r;
+  if ((r = make_tmap(&tw, Qw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N, svdq::kI8KTile, 128,
+                     CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
+    return r;
+  const uint64_t ld = a.M > 1 ? (uint64_t)a.ldy : (uint64_t)a.N;
+  const bool tma_y = ld * sizeof(OT) % 16 == 0;
+  memset(&ty, 0, sizeof(ty));
+  if (tma_y && (r = make_tmap(&ty, a.y, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.N * sizeof(OT), (uint64_t)a.M,
+                              128, 32, CU_TENSOR_MAP_SWIZZLE_128B, ld * sizeof(OT))) != SVDQ_OK)
+    return r;
+  const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = int8_pair_config((int)std::min<int64_t>(tiles, clusters), st, attr);
+  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::svdq_int8_gemm_pair_kernel<OT>, tx, tw, ty, a, tma_y ? 1 : 0));
+  return SVDQ_OK;
+}
+
+template <typename OT>
+svdq_status launch_int8_linear(const svdq::Int8GemmArgs& a, const void* Qx, const void* Qw, cudaStream_t st) {
+  const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+  const int clusters = tiles >= 37 && tiles < (1ll << 31) ? int8_pair_clusters<OT>() : 0;
+  if (clusters > 0) return launch_int8_pair<OT>(a, Qx, Qw, clusters, st);
+  return launch_int8_gemm<128, OT>(a, Qx, Qw, 1, st);
+}
+
 // ---------------------------------------------------------------- norm
 constexpr int64_t kNormMaxC = 16384;
 
@@ -303,7 +369,7 @@ svdq_status svdq_int8_linear(int64_t M, int64_t K, int64_t N, const void* Qx, co
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return with_type(y_dtype, [&](auto tag) -> svdq_status {
     using T = typename decltype(tag)::type;
-    return launch_int8_gemm<128, T>(a, Qx, Qw, 1, st);
+    return launch_int8_linear<T>(a, Qx, Qw, st);
   });
 }
 

@@ -307,4 +307,260 @@ __global__ void __launch_bounds__(kI8Threads) svdq_int8_gemm_kernel(const __grid
   }
 }
 
+// ---------------------------------------------------------------- CTA-pair kernel
+// Large products: one tcgen05 MMA (cta_group::2) spans the two SMs of a cluster
+// of 2 and computes a 256 x 256 tile; each CTA stages its own 128 rows of X and
+// its own 128 rows of W (64 bytes of operands per 1024 multiply-adds and CTA,
+// half of what two single CTAs would fetch). Persistent: cluster c takes tiles
+// c, c + clusters, ...; two accumulators (all 512 columns of tensor memory)
+// alternate, so a tile's epilogue runs under the next tile's MMAs.
+// Roles per CTA (320 threads):
+//   warps 0-7  epilogue: warp (q, h) takes accumulator lanes 32q.. and columns
+//              128h..: scales, bias, rounding, 128B-swizzled boxes, TMA stores
+//   warp 8     producer: TMA loads of this CTA's rows, counted on the even
+//              CTA's stage barrier (64 KB for both)
+//   warp 9     the even CTA's lane 0 issues the MMAs; a multicast commit frees
+//              each stage, and hands over each accumulator, in both CTAs
+// Tiles go in bands of kP8Band tile rows, column by column: the clusters that
+// run at one time then share few rows of X and of W, and L2 serves the rest.
+constexpr int kP8Stages = 5;
+constexpr int kP8StageBytes = 2 * 128 * kI8KTile;            // 32 KB: 128 rows of X, 128 rows of W
+constexpr int kP8Threads = 320;
+constexpr int kP8EpiWarps = 8;
+constexpr int kP8Band = 8;
+constexpr int kP8BoxBytes = 4096;                            // 32 rows x 128 bytes
+constexpr int kP8BoxOffset = kP8Stages * kP8StageBytes;
+constexpr int kP8ColOffset = kP8BoxOffset + kP8EpiWarps * kP8BoxBytes;   // (sw, bias) of each warp's 128 columns
+constexpr int kP8BarOffset = kP8ColOffset + kP8EpiWarps * 128 * 8;
+constexpr int kP8Bytes = kP8BarOffset + 256 + 1024;
+
+__device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// TMA load into this CTA's shared memory, counted on a barrier of the pair's
+// even CTA (`bar`: its shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+      ::"r"(smem_u32(dst)), "l"(tmap), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+struct Int8Tile {
+  int m0, n0;
+};
+
+__device__ __forceinline__ Int8Tile int8_pair_tile(int tile, int tiles_m, int tiles_n) {
+  const int band = tile / (kP8Band * tiles_n);
+  const int rows = min(kP8Band, tiles_m - band * kP8Band);
+  const int i = tile - band * kP8Band * tiles_n;
+  return Int8Tile{(band * kP8Band + i % rows) * 256, (i / rows) * 256};
+}
+
+// tm_y views Y as bytes, in boxes of 32 rows x 128; tma_y = 0 where Y's address or
+// row stride does not allow it (then the staged boxes are written by plain stores).
+template <typename OT>
+__global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x,
+                                                                            const __grid_constant__ CUtensorMap tm_w,
+                                                                            const __grid_constant__ CUtensorMap tm_y,
+                                                                            const Int8GemmArgs a, int tma_y) {
+  extern __shared__ __align__(1024) unsigned char p8_smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(p8_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kP8BarOffset);   // even CTA: both CTAs' loads
+  uint64_t* empty = full + kP8Stages;
+  uint64_t* acc_full = empty + kP8Stages;    // [2]
+  uint64_t* acc_empty = acc_full + 2;        // [2], even CTA: both CTAs' epilogue warps
+  uint64_t* mma_drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const int tiles_m = (a.M + 255) / 256, tiles_n = (a.N + 255) / 256;
+  const int ntiles = tiles_m * tiles_n;
+  const int kts = (a.K + kI8KTile - 1) / kI8KTile;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kP8Stages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + b, 1);
+      mbar_init(acc_empty + b, 2 * kP8EpiWarps);
+    }
+    mbar_init(mma_drain, 1);
+    fence_mbar_init();
+    prefetch_tmap(&tm_x);
+    prefetch_tmap(&tm_w);
+    if (tma_y) prefetch_tmap(&tm_y);
+  }
+  if (warp == 9) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  if (warp == 8) {
+    if (lane == 0) {
+      const uint32_t full_even = mapa_shared(smem_u32(full), 0);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = cluster; tile < ntiles && ok; tile += nclusters) {
+        const Int8Tile t = int8_pair_tile(tile, tiles_m, tiles_n);
+        for (int kt = 0; kt < kts; ++kt, ++it) {
+          const uint32_t s = it % kP8Stages;
+          if (!mbar_wait(empty + s, ((it / kP8Stages) & 1u) ^ 1u, kDevErrTimeoutEmpty)) {
+            ok = false;
+            break;
+          }
+          unsigned char* sa = smem + s * kP8StageBytes;
+          if (crank == 0) mbar_arrive_expect_tx(full + s, 2 * kP8StageBytes);
+          tma_load_2d_pair(sa, &tm_x, full_even + 8 * s, kt * kI8KTile, t.m0 + 128 * (int)crank);
+          tma_load_2d_pair(sa + kP8StageBytes / 2, &tm_w, full_even + 8 * s, kt * kI8KTile, t.n0 + 128 * (int)crank);
+        }
+      }
+      // After a failure, let this thread's loads land before the CTAs exit. The
+      // odd CTA's are counted in the other CTA, so both wait a time that no load
+      // in flight can outlast.
+      if (device_error_set()) {
+        const unsigned long long t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {
+        }
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0 && crank == 0) {
+      const uint32_t idesc = idesc_i8(256, 256);
+      const uint64_t dA0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+      const uint64_t dB0 = smem_desc(smem_u32(smem) + kP8StageBytes / 2, 16, 1024, kSwizzle128B);
+      uint32_t it = 0, tcount = 0;
+      bool ok = true;
+      for (int tile = cluster; tile < ntiles && ok; tile += nclusters, ++tcount) {
+        const uint32_t buf = tcount & 1u;
+        if (!mbar_wait(acc_empty + buf, ((tcount >> 1) & 1u) ^ 1u, kDevErrTimeoutAccum)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int kt = 0; kt < kts; ++kt, ++it) {
+          const uint32_t s = it % kP8Stages;
+          if (!mbar_wait(full + s, (it / kP8Stages) & 1u, kDevErrTimeoutFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t off = (uint64_t)(s * ((uint32_t)kP8StageBytes >> 4));
+#pragma unroll
+          for (int j = 0; j < kI8KTile / 32; ++j)
+            mma_i8_pair(tmem + 256 * buf, dA0 + off + 2u * j, dB0 + off + 2u * j, idesc, (kt | j) != 0 ? 1u : 0u);
+          tc_commit_pair(empty + s, 0x3);
+        }
+        if (ok) tc_commit_pair(acc_full + buf, 0x3);
+      }
+      if (!ok) {
+        tc_commit_pair(mma_drain, 0x1);
+        mbar_drain(mma_drain, 0);
+      }
+    }
+  } else {
+    const int q = warp & 3, h = warp >> 2;
+    unsigned char* box = smem + kP8BoxOffset + warp * kP8BoxBytes;
+    float2* colv = reinterpret_cast<float2*>(smem + kP8ColOffset) + warp * 128;
+    const uint32_t acc_empty_even = mapa_shared(smem_u32(acc_empty), 0);
+    constexpr int kBoxCols = 128 / (int)sizeof(OT);
+    uint32_t tcount = 0;
+    for (int tile = cluster; tile < ntiles; tile += nclusters, ++tcount) {
+      const Int8Tile t = int8_pair_tile(tile, tiles_m, tiles_n);
+      const uint32_t buf = tcount & 1u;
+      const int m0 = t.m0 + 128 * (int)crank + 32 * q, n0 = t.n0 + 128 * h;
+      const float sx = m0 + lane < a.M ? a.sx[m0 + lane] : 0.f;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + 32 * i + lane;
+        colv[32 * i + lane] = n < a.N ? make_float2(a.sw[n], a.bias ? a.bias[n] : 0.f) : make_float2(0.f, 0.f);
+      }
+      __syncwarp();
+      bool ok = mbar_wait(acc_full + buf, (tcount >> 1) & 1u, kDevErrTimeoutAccum) && !device_error_set();
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      tc_fence_after();
+      if (!ok) break;
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + 256 * buf + (uint32_t)(h * 128);
+      const bool live = m0 < a.M;
+#pragma unroll
+      for (int b = 0; b < 128 / kBoxCols; ++b) {
+        if (tma_y && lane == 0) bulk_wait_read<0>();   // the previous store from this box has read it
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < kBoxCols; c += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(taddr + b * kBoxCols + c, v);
+          tmem_ld_wait();
+          if (b * kBoxCols + c + 32 == 128) {   // the accumulator is drained
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
+          }
+          float f[32];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float4 sb = *reinterpret_cast<const float4*>(colv + b * kBoxCols + c + i);
+            f[i] = fmaf((float)(int)v[i] * sb.x, sx, sb.y);
+            f[i + 1] = fmaf((float)(int)v[i + 1] * sb.z, sx, sb.w);
+          }
+          // row `lane` of the box: 16-byte chunk j at (j ^ (lane & 7)), the 128B swizzle
+          constexpr int kChunks = 32 * (int)sizeof(OT) / 16;
+#pragma unroll
+          for (int j = 0; j < kChunks; ++j) {
+            float g[kVecN<OT>];
+#pragma unroll
+            for (int i = 0; i < kVecN<OT>; ++i) g[i] = f[j * kVecN<OT> + i];
+            const int chunk = c * (int)sizeof(OT) / 16 + j;
+            *reinterpret_cast<uint4*>(box + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = pack_vec<OT>(g);
+          }
+        }
+        const int col0 = n0 + b * kBoxCols;
+        if (tma_y) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && live && col0 < a.N) {
+            tma_store_2d_evict_first(&tm_y, box, col0 * (int)sizeof(OT), m0);   // x in bytes
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+          const int rows = min(32, a.M - m0);
+          for (int r = 0; r < rows; ++r)
+#pragma unroll
+            for (int c = 0; c < kBoxCols; c += 32) {
+              const int e = c + lane, byte = e * (int)sizeof(OT);
+              const OT value = *reinterpret_cast<const OT*>(box + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
+              if (col0 + e < a.N) static_cast<OT*>(a.y)[(long long)(m0 + r) * a.ldy + col0 + e] = value;
+            }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait<0>();
+  }
+  tc_fence_before();
+  cluster_sync();   // no CTA leaves while its peer may still signal its barriers
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 }  // namespace svdq
