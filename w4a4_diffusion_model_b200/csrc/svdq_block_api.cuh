@@ -41,6 +41,11 @@ struct Tag {
   using type = T;
 };
 
+template <auto K>
+struct Kern {
+  static constexpr auto value = K;
+};
+
 template <typename F>
 svdq_status with_type(int dtype, F&& f) {
   switch (dtype) {
@@ -48,6 +53,33 @@ svdq_status with_type(int dtype, F&& f) {
     case SVDQ_FP16: return f(Tag<__half>());
     default: return f(Tag<float>());
   }
+}
+
+int round_up(int v, int m) { return (v + m - 1) / m * m; }
+
+// Kernels that stream rows through a ring (svdq_rows.cuh): stages for about
+// 48 KB of rows a block, at least one and at most kRingMaxStages of them.
+constexpr int kRingMaxBytes = 2 * 65536;   // one stage of two rows of 16384 fp32
+
+int ring_depth(size_t stage_bytes) {
+  return (int)std::max<size_t>(1, std::min<size_t>(svdq::kRingMaxStages, 49152 / stage_bytes));
+}
+
+// Resident blocks per SM of a ring kernel; sets its shared-memory attribute.
+template <auto KERN>
+int ring_blocks_per_sm(int threads, size_t smem) {
+  static std::atomic<int> done[kMaxDevices];
+  per_device_once(done, current_device(), [] {
+    if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMaxBytes) == cudaSuccess) return 1;
+    cudaGetLastError();
+    return 0;
+  });
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERN, threads, smem) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  return std::max(n, 1);
 }
 
 // ---------------------------------------------------------------- 8-bit quantizer
@@ -68,8 +100,6 @@ svdq_status launch_int8_quantize(const svdq::Int8QuantArgs& a, dim3 grid, dim3 b
   return SVDQ_OK;
 }
 
-int round_up(int v, int m) { return (v + m - 1) / m * m; }
-
 svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_t ldx, const float* mult, void* Q,
                           float* S, void* stream) {
   g_last_error[0] = 0;
@@ -83,7 +113,7 @@ svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_
     return fail(SVDQ_ERR_MISALIGNED, "row stride %lld is not a multiple of 16 bytes", (long long)ldx);
   if ((r = check_device()) != SVDQ_OK) return r;
   if (M == 0) return SVDQ_OK;
-  const svdq::Int8QuantArgs a{X, ldx, mult, static_cast<int8_t*>(Q), S, M, (int)K};
+  svdq::Int8QuantArgs a{X, ldx, mult, static_cast<int8_t*>(Q), S, M, (int)K, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return with_type(dtype, [&](auto tag) -> svdq_status {
     using T = typename decltype(tag)::type;
@@ -95,6 +125,21 @@ svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_
       if (vecs <= 32) return launch_int8_quantize<T, 1, 256>(a, grid, block, st);
       if (vecs <= 64) return launch_int8_quantize<T, 2, 256>(a, grid, block, st);
       return launch_int8_quantize<T, 4, 256>(a, grid, block, st);
+    }
+    if (K <= 16384 && M > 2 * sms) {
+      const size_t row = (size_t)K * sizeof(T);
+      a.depth = ring_depth(row);
+      const int threads = round_up((int)(K / svdq::kRowElems), 32);
+      auto go = [&](auto kern_c) -> svdq_status {
+        constexpr auto kern = decltype(kern_c)::value;
+        const int64_t blocks = sms * ring_blocks_per_sm<kern>(threads, a.depth * row);
+        cudaLaunchAttribute attr[1];
+        cudaLaunchConfig_t cfg = pdl_config((unsigned)std::min<int64_t>(M, blocks), threads, a.depth * row, st, attr);
+        SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
+        return SVDQ_OK;
+      };
+      if (threads <= 512) return go(Kern<svdq::int8_quantize_rows_kernel<T, 512>>());
+      return go(Kern<svdq::int8_quantize_rows_kernel<T, 1024>>());
     }
     const unsigned grid = (unsigned)std::min<int64_t>(M, sms * 8);
     if (vecs <= 512) return launch_int8_quantize<T, 2, 256>(a, grid, round_up((vecs + 1) / 2, 32), st);
@@ -279,6 +324,24 @@ svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStr
     using WT = typename decltype(wtag)::type;
     constexpr bool VEC = decltype(vec)::value;
     const int pieces = (int)n.C / (VEC ? svdq::kVecN<T> : 1);
+    if constexpr (VEC) {
+      const int threads = round_up(((int)n.C + svdq::kRowElems - 1) / svdq::kRowElems, 32);
+      if (threads > 32 && n.M > 2 * sm_count()) {
+        svdq::NormArgs r = a;
+        const size_t row = (size_t)n.C * sizeof(T);
+        r.depth = ring_depth(row);
+        auto go = [&](auto kern_c) -> svdq_status {
+          constexpr auto kern = decltype(kern_c)::value;
+          const int64_t blocks = (int64_t)sm_count() * ring_blocks_per_sm<kern>(threads, r.depth * row);
+          cudaLaunchAttribute attr[1];
+          cudaLaunchConfig_t cfg = pdl_config((unsigned)std::min<int64_t>(n.M, blocks), threads, r.depth * row, st, attr);
+          SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, r));
+          return SVDQ_OK;
+        };
+        if (threads <= 512) return go(Kern<svdq::layernorm_rows_kernel<T, WT, 512, QUANT>>());
+        return go(Kern<svdq::layernorm_rows_kernel<T, WT, 1024, QUANT>>());
+      }
+    }
     return norm_width<VEC>(pieces, [&](auto nv, auto maxt) -> svdq_status {
       constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
       const int threads = round_up((pieces + NV - 1) / NV, 32);
@@ -465,6 +528,23 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
     using WT = typename decltype(wtag)::type;
     constexpr bool VEC = decltype(vec)::value;
     const int pieces = (int)n.C / (VEC ? svdq::kVecN<T> : 1);
+    if constexpr (VEC) {
+      const int threads = round_up(((int)n.C + svdq::kRowElems - 1) / svdq::kRowElems, 32);
+      if (threads > 32) {
+        const size_t rows = 2 * (size_t)n.C * sizeof(T);
+        a.depth = ring_depth(rows);
+        auto go = [&](auto kern_c) -> svdq_status {
+          constexpr auto kern = decltype(kern_c)::value;
+          ring_blocks_per_sm<kern>(threads, a.depth * rows);
+          cudaLaunchAttribute attr[1];
+          cudaLaunchConfig_t cfg = pdl_config((unsigned)(groups * a.chunks), threads, a.depth * rows, st, attr);
+          SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
+          return SVDQ_OK;
+        };
+        if (threads <= 512) return go(Kern<svdq::layernorm_backward_rows_kernel<T, WT, 512>>());
+        return go(Kern<svdq::layernorm_backward_rows_kernel<T, WT, 1024>>());
+      }
+    }
     return norm_width<VEC>(pieces, [&](auto nv, auto maxt) -> svdq_status {
       constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
       constexpr int N = VEC ? svdq::kVecN<T> : 1;

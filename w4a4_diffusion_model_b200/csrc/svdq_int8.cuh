@@ -11,6 +11,7 @@
 
 #include "svdq_int8_codec.cuh"
 #include "svdq_ptx.cuh"
+#include "svdq_rows.cuh"
 #include "svdq_vec.cuh"
 
 namespace svdq {
@@ -24,6 +25,7 @@ struct Int8QuantArgs {
   float* s;             // [M]
   long long M;
   int K;
+  int depth;            // stages of the row ring
 };
 
 template <typename T>
@@ -42,7 +44,7 @@ __device__ __forceinline__ void int8_values(const Int8QuantArgs& a, const uint4&
 // write of the codes, which is the bound (HBM). NV = 0: the row does not fit;
 // it is read once for its maximum and once more, from L2, for its codes.
 template <typename T, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) int8_quantize_kernel(const Int8QuantArgs a) {
+__global__ void __launch_bounds__(MAXT, 1) int8_quantize_kernel(const Int8QuantArgs a) {
   constexpr int N = kVecN<T>;
   constexpr int R = NV ? NV : 1;
   __shared__ float2 slots[2][32];
@@ -96,6 +98,67 @@ __global__ void __launch_bounds__(MAXT) int8_quantize_kernel(const Int8QuantArgs
         int8_store<N>(q + k, f, sc);
       }
     }
+  }
+}
+
+// Many rows of more than one warp: a block per row, rows streamed through the ring.
+template <typename T, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) int8_quantize_rows_kernel(const Int8QuantArgs a) {
+  constexpr int N = kVecN<T>, NV = kRowPieces<T>;
+  extern __shared__ __align__(16) unsigned char quant_ring[];
+  __shared__ float2 slots[2][32];
+  __shared__ uint64_t full[kRingMaxStages];
+  const int warps = blockDim.x >> 5, tid = threadIdx.x;
+  RowRing<1> ring = {quant_ring, full, {static_cast<const unsigned char*>(a.x)}, {a.ldx * (long long)sizeof(T)},
+                     (uint32_t)(a.K * (int)sizeof(T)), a.depth};
+  if (tid == 0) ring.init();
+  __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (tid == 0)
+    for (int s = 0; s < a.depth; ++s) {
+      const long long m = blockIdx.x + (long long)s * gridDim.x;
+      if (m < a.M) ring.fetch(s, m);
+    }
+  bool in[NV];
+  float l[NV][N];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int k = (v * (int)blockDim.x + tid) * N;
+    in[v] = k < a.K;
+    if (a.mult && in[v]) {
+      load_params<float, N>(a.mult + k, l[v]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) l[v][i] = 1.f;
+    }
+  }
+  int stage = 0, turn = 0;
+  uint32_t parity = 0;
+  for (long long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+    ring.wait(stage, parity);
+    float f[NV][N], amax = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (in[v]) {
+        unpack_vec<T>(*reinterpret_cast<const uint4*>(ring.row(stage, 0) + (v * (int)blockDim.x + tid) * 16), f[v]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          f[v][i] *= l[v][i];
+          amax = max_nan(amax, fabsf(f[v][i]));
+        }
+      }
+    amax = team_max_nan(amax, warps, slots[turn]);
+    if (tid == 0 && m + (long long)a.depth * gridDim.x < a.M) ring.fetch(stage, m + (long long)a.depth * gridDim.x);
+    if (++stage == a.depth) {
+      stage = 0;
+      parity ^= 1u;
+    }
+    const Int8Scale sc = int8_scale(amax);
+    if (tid == 0) a.s[m] = sc.s;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (in[v]) int8_store<N>(a.q + m * a.K + (v * (int)blockDim.x + tid) * N, f[v], sc);
   }
 }
 

@@ -17,6 +17,7 @@
 
 #include "svdq_int8_codec.cuh"
 #include "svdq_ptx.cuh"
+#include "svdq_rows.cuh"
 #include "svdq_vec.cuh"
 
 namespace svdq {
@@ -47,6 +48,7 @@ struct NormArgs {
   float* db;
   float* part;           // [chunks][2][groups][C] partial sums of dw and db, null: one chunk, straight to dw and db
   int chunks;            // row chunks per group
+  int depth;             // stages of the row ring
 };
 
 template <typename WT, int N>
@@ -65,7 +67,7 @@ __device__ __forceinline__ void norm_gain(const NormArgs& a, long long g, int c,
 // in the block: blockDim.y) or the whole block (blockDim.y == 1). A thread
 // holds NV pieces of the row.
 template <typename T, typename WT, int NV, int MAXT, bool VEC, bool QUANT>
-__global__ void __launch_bounds__(MAXT) layernorm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(MAXT, 1) layernorm_kernel(const NormArgs a) {
   using P = Piece<T, VEC>;
   constexpr int N = P::kN;
   __shared__ float2 slots[3][32];
@@ -153,12 +155,140 @@ __global__ void __launch_bounds__(MAXT) layernorm_kernel(const NormArgs a) {
   }
 }
 
+// Forward for rows of more than one warp: a block per row, rows streamed through
+// the ring, weight and bias of the group kept in registers. Thread t holds the
+// pieces t, t + blockDim.x, ... of a row (kRowElems values).
+//
+// Mean and variance take one barrier: each warp forms its own mean and its own
+// sum of squares around that mean, and the block joins them,
+//   M2 = sum_w (M2_w + n_w (mean_w - mean)^2).
+template <typename T, typename WT, int MAXT, bool QUANT>
+__global__ void __launch_bounds__(MAXT, 1) layernorm_rows_kernel(const NormArgs a) {
+  constexpr int N = kVecN<T>, NV = kRowPieces<T>;
+  extern __shared__ __align__(16) unsigned char norm_ring[];
+  __shared__ float2 slots[2][32];
+  __shared__ float2 counts[32];                  // n_w and 1 / n_w
+  __shared__ uint64_t full[kRingMaxStages];
+  const int warps = blockDim.x >> 5, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float inv_c = 1.f / (float)a.C;
+  RowRing<1> ring = {norm_ring, full, {static_cast<const unsigned char*>(a.x)}, {a.ldx * (long long)sizeof(T)},
+                     (uint32_t)(a.C * (int)sizeof(T)), a.depth};
+  if (tid == 0) ring.init();
+  bool in[NV];
+  int mine = 0;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    in[v] = (v * (int)blockDim.x + tid) * N < a.C;
+    mine += in[v] ? N : 0;
+  }
+  mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+  if (lane == 0) counts[warp] = make_float2((float)mine, mine ? 1.f / (float)mine : 0.f);
+  __syncthreads();
+  const float inv_n = counts[warp].y;
+  const float lane_n = lane < warps ? counts[lane].x : 0.f, lane_inv_n = lane < warps ? counts[lane].y : 0.f;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (tid == 0)
+    for (int s = 0; s < a.depth; ++s) {
+      const long long m = blockIdx.x + (long long)s * gridDim.x;
+      if (m < a.M) ring.fetch(s, m);
+    }
+  float w[NV][N], b[NV][N];
+  long long group = -1;
+  int stage = 0, turn = 0;
+  uint32_t parity = 0;
+  for (long long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+    const long long g = (unsigned)m / (unsigned)a.rows_per_group;
+    if (g != group) {
+      group = g;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = (v * (int)blockDim.x + tid) * N;
+        if (in[v]) {
+          norm_gain<WT, N>(a, g, c, w[v]);
+          if (a.b) load_params<WT, N>(static_cast<const WT*>(a.b) + g * a.C + c, b[v]);
+        }
+        if (!a.b) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) b[v][i] = 0.f;
+        }
+      }
+    }
+    ring.wait(stage, parity);
+    float f[NV][N], sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint4 r = in[v] ? *reinterpret_cast<const uint4*>(ring.row(stage, 0) + (v * (int)blockDim.x + tid) * 16)
+                            : make_uint4(0, 0, 0, 0);
+      unpack_vec<T>(r, f[v]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum += f[v][i];
+    }
+    sum = warp_sum(sum);
+    const float own = sum * inv_n;
+    float sq = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (in[v]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) sq = fmaf(f[v][i] - own, f[v][i] - own, sq);
+      }
+    sq = warp_sum(sq);
+    if (lane == 0) slots[turn][warp] = make_float2(sum, sq);
+    __syncthreads();
+    if (tid == 0 && m + (long long)a.depth * gridDim.x < a.M) ring.fetch(stage, m + (long long)a.depth * gridDim.x);
+    const float2 t = lane < warps ? slots[turn][lane] : make_float2(0.f, 0.f);
+    const float mean = warp_sum(t.x) * inv_c;
+    const float d = t.x * lane_inv_n - mean;
+    const float rstd = 1.f / sqrtf(warp_sum(fmaf(lane_n * d, d, t.y)) * inv_c + a.eps);
+    if (++stage == a.depth) {
+      stage = 0;
+      parity ^= 1u;
+    }
+    if (tid == 0) {
+      if (a.mean) a.mean[m] = mean;
+      if (a.rstd) a.rstd[m] = rstd;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[v][i] = fmaf((f[v][i] - mean) * rstd, w[v][i], b[v][i]);
+    if constexpr (!QUANT) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (in[v]) Piece<T, true>::store(static_cast<T*>(a.y) + m * a.ldy + (v * (int)blockDim.x + tid) * N, f[v]);
+    } else {
+      float amax = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (in[v]) {
+          if (a.inv_lambda) {
+            float l[N];
+            load_params<float, N>(a.inv_lambda + (v * (int)blockDim.x + tid) * N, l);
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[v][i] *= l[i];
+          }
+#pragma unroll
+          for (int i = 0; i < N; ++i) amax = max_nan(amax, fabsf(f[v][i]));
+        }
+      __shared__ float2 tops[2][32];
+      const Int8Scale sc = int8_scale(team_max_nan(amax, warps, tops[turn]));
+      if (tid == 0) a.s[m] = sc.s;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = (v * (int)blockDim.x + tid) * N;
+        if (in[v]) int8_store<N>(a.q + m * a.C + c, f[v], sc);
+      }
+    }
+  }
+}
+
 // Backward. blockIdx.x = group * chunks + chunk; a block's teams (blockDim.y of
 // them) take the chunk's rows in turn and add dy xhat and dy of their columns
 // in registers; the block then adds its teams' sums in team order and writes
 // one partial row of dw and db. Every order is fixed, so are the results.
 template <typename T, typename WT, int NV, int MAXT, bool VEC>
-__global__ void __launch_bounds__(MAXT) layernorm_backward_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormArgs a) {
   using P = Piece<T, VEC>;
   constexpr int N = P::kN;
   extern __shared__ float norm_smem[];      // [NV * N][blockDim.x]: the teams' sums, one team at a time
@@ -286,6 +416,104 @@ __global__ void __launch_bounds__(MAXT) layernorm_backward_kernel(const NormArgs
       }
     }
   }
+}
+
+// Backward for rows of more than one warp: as above with one team, the rows of
+// x and dy streamed through the ring.
+template <typename T, typename WT, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1) layernorm_backward_rows_kernel(const NormArgs a) {
+  constexpr int N = kVecN<T>, NV = kRowPieces<T>;
+  extern __shared__ __align__(16) unsigned char norm_ring[];
+  __shared__ float2 slots[2][32];
+  __shared__ uint64_t full[kRingMaxStages];
+  const int warps = blockDim.x >> 5, tid = threadIdx.x;
+  const float inv_c = 1.f / (float)a.C;
+  RowRing<2> ring = {norm_ring, full,
+                     {static_cast<const unsigned char*>(a.x), static_cast<const unsigned char*>(a.dy)},
+                     {a.ldx * (long long)sizeof(T), a.lddy * (long long)sizeof(T)},
+                     (uint32_t)(a.C * (int)sizeof(T)), a.depth};
+  if (tid == 0) ring.init();
+  const long long g = blockIdx.x / a.chunks, groups = gridDim.x / a.chunks;
+  const int chunk = (int)(blockIdx.x % a.chunks);
+  const long long row0 = g * a.rows_per_group, rows = min(a.rows_per_group, a.M - row0);
+  bool in[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) in[v] = (v * (int)blockDim.x + tid) * N < a.C;
+  __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (tid == 0)
+    for (int s = 0; s < a.depth; ++s) {
+      const long long k = chunk + (long long)s * a.chunks;
+      if (k < rows) ring.fetch(s, row0 + k);
+    }
+  float w[NV][N], dw[NV][N], db[NV][N];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if (in[v]) norm_gain<WT, N>(a, g, (v * (int)blockDim.x + tid) * N, w[v]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[v][i] = db[v][i] = 0.f;
+  }
+  int stage = 0, turn = 0;
+  uint32_t parity = 0;
+  float mean = 0.f, rstd = 0.f;
+  if (chunk < rows) {
+    mean = a.mean[row0 + chunk];
+    rstd = a.rstd[row0 + chunk];
+  }
+  for (long long k = chunk; k < rows; k += a.chunks, turn ^= 1) {
+    // the next row's statistics, ahead of their use
+    const long long next = min(k + a.chunks, rows - 1);
+    const float mean1 = a.mean[row0 + next], rstd1 = a.rstd[row0 + next];
+    ring.wait(stage, parity);
+    float xh[NV][N], h[NV][N], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (in[v]) {
+        unpack_vec<T>(*reinterpret_cast<const uint4*>(ring.row(stage, 0) + (v * (int)blockDim.x + tid) * 16), xh[v]);
+        unpack_vec<T>(*reinterpret_cast<const uint4*>(ring.row(stage, 1) + (v * (int)blockDim.x + tid) * 16), h[v]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          xh[v][i] = (xh[v][i] - mean) * rstd;
+          dw[v][i] = fmaf(h[v][i], xh[v][i], dw[v][i]);
+          db[v][i] += h[v][i];
+          h[v][i] *= w[v][i];
+          s1 += h[v][i];
+          s2 = fmaf(h[v][i], xh[v][i], s2);
+        }
+      }
+    }
+    const float2 s = team_sum2(s1, s2, warps, slots[turn]);
+    if (tid == 0 && k + (long long)a.depth * a.chunks < rows) ring.fetch(stage, row0 + k + (long long)a.depth * a.chunks);
+    if (++stage == a.depth) {
+      stage = 0;
+      parity ^= 1u;
+    }
+    const float m1 = s.x * inv_c, m2 = s.y * inv_c;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (in[v]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) h[v][i] = rstd * (h[v][i] - m1 - xh[v][i] * m2);
+        Piece<T, true>::store(static_cast<T*>(a.dx) + (row0 + k) * a.lddx + (v * (int)blockDim.x + tid) * N, h[v]);
+      }
+    mean = mean1;
+    rstd = rstd1;
+  }
+  if (!a.dw && !a.db) return;
+  const long long cols = groups * a.C;
+  float* pw = a.part ? a.part + 2ll * chunk * cols : a.dw;
+  float* pb = a.part ? a.part + (2ll * chunk + 1) * cols : a.db;
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    if (in[v]) {
+      const long long c = g * a.C + (v * (int)blockDim.x + tid) * N;
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        if (pw) *reinterpret_cast<float4*>(pw + c + i) = make_float4(dw[v][i], dw[v][i + 1], dw[v][i + 2], dw[v][i + 3]);
+        if (pb) *reinterpret_cast<float4*>(pb + c + i) = make_float4(db[v][i], db[v][i + 1], db[v][i + 2], db[v][i + 3]);
+      }
+    }
 }
 
 // dw and db from the chunks' partial rows: a block takes 32 columns, its warp
