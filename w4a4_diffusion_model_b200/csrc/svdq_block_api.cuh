@@ -59,7 +59,7 @@ int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
 // Kernels that stream rows through a ring (svdq_rows.cuh): stages for about
 // 48 KB of rows a block, at least one and at most kRingMaxStages of them.
-constexpr int kRingMaxBytes = 2 * 65536;   // one stage of two rows of 16384 fp32
+constexpr int kRingMaxBytes = 3 * 65536;   // one stage of two rows of 16384 fp32, and the backward pass's weight
 
 int ring_depth(size_t stage_bytes) {
   return (int)std::max<size_t>(1, std::min<size_t>(svdq::kRingMaxStages, 49152 / stage_bytes));
@@ -80,6 +80,18 @@ int ring_blocks_per_sm(int threads, size_t smem) {
     n = 0;
   }
   return std::max(n, 1);
+}
+
+// Launches a ring kernel that takes rows in turn, `elems` elements a thread.
+template <auto KERN, typename Args>
+svdq_status launch_rows(const Args& a, int64_t rows, int64_t cols, int elems, size_t row_bytes, cudaStream_t st) {
+  const int threads = round_up((int)((cols + elems - 1) / elems), 32);
+  const size_t smem = a.depth * row_bytes;
+  const int64_t blocks = (int64_t)sm_count() * ring_blocks_per_sm<KERN>(threads, smem);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pdl_config((unsigned)std::min<int64_t>(rows, blocks), threads, smem, st, attr);
+  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, KERN, a));
+  return SVDQ_OK;
 }
 
 // ---------------------------------------------------------------- 8-bit quantizer
@@ -127,19 +139,13 @@ svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_
       return launch_int8_quantize<T, 4, 256>(a, grid, block, st);
     }
     if (K <= 16384 && M > 2 * sms) {
+      using namespace svdq;
+      a.depth = ring_depth((size_t)K * sizeof(T));
       const size_t row = (size_t)K * sizeof(T);
-      a.depth = ring_depth(row);
-      const int threads = round_up((int)(K / svdq::kRowElems), 32);
-      auto go = [&](auto kern_c) -> svdq_status {
-        constexpr auto kern = decltype(kern_c)::value;
-        const int64_t blocks = sms * ring_blocks_per_sm<kern>(threads, a.depth * row);
-        cudaLaunchAttribute attr[1];
-        cudaLaunchConfig_t cfg = pdl_config((unsigned)std::min<int64_t>(M, blocks), threads, a.depth * row, st, attr);
-        SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
-        return SVDQ_OK;
-      };
-      if (threads <= 512) return go(Kern<svdq::int8_quantize_rows_kernel<T, 512>>());
-      return go(Kern<svdq::int8_quantize_rows_kernel<T, 1024>>());
+      if (K <= 2048) return launch_rows<int8_quantize_rows_kernel<T, 16, 4>>(a, M, K, 16, row, st);
+      if (K <= 4096) return launch_rows<int8_quantize_rows_kernel<T, 32, 4>>(a, M, K, 32, row, st);
+      if (K <= 8192) return launch_rows<int8_quantize_rows_kernel<T, 32, 8>>(a, M, K, 32, row, st);
+      return launch_rows<int8_quantize_rows_kernel<T, 32, 16>>(a, M, K, 32, row, st);
     }
     const unsigned grid = (unsigned)std::min<int64_t>(M, sms * 8);
     if (vecs <= 512) return launch_int8_quantize<T, 2, 256>(a, grid, round_up((vecs + 1) / 2, 32), st);
@@ -325,21 +331,15 @@ svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStr
     constexpr bool VEC = decltype(vec)::value;
     const int pieces = (int)n.C / (VEC ? svdq::kVecN<T> : 1);
     if constexpr (VEC) {
-      const int threads = round_up(((int)n.C + svdq::kRowElems - 1) / svdq::kRowElems, 32);
-      if (threads > 32 && n.M > 2 * sm_count()) {
-        svdq::NormArgs r = a;
+      if (n.C > 512 && n.M > 2 * sm_count()) {
+        using namespace svdq;
+        NormArgs r = a;
         const size_t row = (size_t)n.C * sizeof(T);
         r.depth = ring_depth(row);
-        auto go = [&](auto kern_c) -> svdq_status {
-          constexpr auto kern = decltype(kern_c)::value;
-          const int64_t blocks = (int64_t)sm_count() * ring_blocks_per_sm<kern>(threads, r.depth * row);
-          cudaLaunchAttribute attr[1];
-          cudaLaunchConfig_t cfg = pdl_config((unsigned)std::min<int64_t>(n.M, blocks), threads, r.depth * row, st, attr);
-          SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, r));
-          return SVDQ_OK;
-        };
-        if (threads <= 512) return go(Kern<svdq::layernorm_rows_kernel<T, WT, 512, QUANT>>());
-        return go(Kern<svdq::layernorm_rows_kernel<T, WT, 1024, QUANT>>());
+        if (n.C <= 2048) return launch_rows<layernorm_rows_kernel<T, WT, 16, 4, QUANT>>(r, n.M, n.C, 16, row, st);
+        if (n.C <= 4096) return launch_rows<layernorm_rows_kernel<T, WT, 32, 4, QUANT>>(r, n.M, n.C, 32, row, st);
+        if (n.C <= 8192) return launch_rows<layernorm_rows_kernel<T, WT, 32, 8, QUANT>>(r, n.M, n.C, 32, row, st);
+        return launch_rows<layernorm_rows_kernel<T, WT, 32, 16, QUANT>>(r, n.M, n.C, 32, row, st);
       }
     }
     return norm_width<VEC>(pieces, [&](auto nv, auto maxt) -> svdq_status {
@@ -355,12 +355,13 @@ svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStr
   });
 }
 
-// Row chunks per group of the backward pass: about two blocks per SM over all
-// groups. More groups than that: each block takes a group's rows alone, and no
-// partial sums are kept.
+// Row chunks per group of the backward pass: blocks of about 640 threads in all
+// per SM (16 channels a thread), over all groups. More groups than that: each
+// block takes a group's rows alone, and no partial sums are kept.
 int64_t norm_chunks(const NormCall& n) {
   const int64_t groups = norm_groups(n);
-  const int64_t per = std::max<int64_t>(1, 2ll * sm_count() / groups);
+  const int64_t per_sm = n.C <= 512 ? 2 : std::max<int64_t>(1, 640 / round_up((int)(n.C + 15) / 16, 32));
+  const int64_t per = std::max<int64_t>(1, per_sm * sm_count() / groups);
   return std::min<int64_t>(per, std::max<int64_t>(1, (norm_group_rows(n) + 3) / 4));
 }
 
@@ -376,13 +377,17 @@ svdq_status launch_rope(svdq::RopeArgs a, bool halves, cudaStream_t st) {
   bool vec = (a.D - a.R) % V == 0 && (halves ? a.R / 2 : a.R) % V == 0 && a.D % V == 0;
   if (a.T > 1) vec = vec && a.xt % V == 0 && a.yt % V == 0;
   if (a.heads > 1) vec = vec && a.xh % V == 0 && a.yh % V == 0;
-  // few tokens: several blocks share a token's heads
-  const int64_t want = 4ll * sm_count();
-  const int shares = (int)std::min<int64_t>(std::min<int64_t>(a.heads, 65535), std::max<int64_t>(1, want / a.T));
+  // Enough blocks for every SM come first: few tokens share their heads among
+  // several blocks, many go together so that their angles fill the block.
+  const int64_t want = 8ll * sm_count();
+  const int shares = (int)std::min<int64_t>(a.heads, std::max<int64_t>(1, want / a.T));
   a.heads_per_block = (a.heads + shares - 1) / shares;
-  const dim3 grid((unsigned)std::min<int64_t>(a.T, 1ll << 30), (unsigned)((a.heads + a.heads_per_block - 1) / a.heads_per_block));
-  const int items = a.heads_per_block * (a.D / (vec ? (halves ? 2 * V : V) : 2));
-  const int threads = std::min(256, round_up(items, 32));
+  a.tokens_per_block = (int)std::max<int64_t>(
+      1, std::min<int64_t>({a.T / want, (int64_t)svdq::kRopeTable / (a.R / 2), (int64_t)svdq::kRopeThreads / (a.R / 2)}));
+  const dim3 grid((unsigned)((a.T + a.tokens_per_block - 1) / a.tokens_per_block),
+                  (unsigned)((a.heads + a.heads_per_block - 1) / a.heads_per_block));
+  const int items = a.heads_per_block * (vec ? (a.R / (halves ? 2 * V : V) + (a.D - a.R) / V) : a.D - a.R / 2);
+  const int threads = std::min(svdq::kRopeThreads, round_up(std::max(items, a.R / 2), 32));
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = pdl_config(grid, threads, 0, st, attr);
   if (halves) {
@@ -529,20 +534,23 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
     constexpr bool VEC = decltype(vec)::value;
     const int pieces = (int)n.C / (VEC ? svdq::kVecN<T> : 1);
     if constexpr (VEC) {
-      const int threads = round_up(((int)n.C + svdq::kRowElems - 1) / svdq::kRowElems, 32);
-      if (threads > 32) {
+      if (n.C > 512) {
+        using namespace svdq;
         const size_t rows = 2 * (size_t)n.C * sizeof(T);
         a.depth = ring_depth(rows);
-        auto go = [&](auto kern_c) -> svdq_status {
+        auto go = [&](auto kern_c, int elems) -> svdq_status {
           constexpr auto kern = decltype(kern_c)::value;
-          ring_blocks_per_sm<kern>(threads, a.depth * rows);
+          const int threads = round_up(((int)n.C + elems - 1) / elems, 32);
+          const size_t smem = a.depth * rows + (size_t)n.C * 4;
+          ring_blocks_per_sm<kern>(threads, smem);   // sets the attribute
           cudaLaunchAttribute attr[1];
-          cudaLaunchConfig_t cfg = pdl_config((unsigned)(groups * a.chunks), threads, a.depth * rows, st, attr);
+          cudaLaunchConfig_t cfg = pdl_config((unsigned)(groups * a.chunks), threads, smem, st, attr);
           SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
           return SVDQ_OK;
         };
-        if (threads <= 512) return go(Kern<svdq::layernorm_backward_rows_kernel<T, WT, 512>>());
-        return go(Kern<svdq::layernorm_backward_rows_kernel<T, WT, 1024>>());
+        if (n.C <= 5120) return go(Kern<layernorm_backward_rows_kernel<T, WT, 16, 10, 2, true>>(), 16);
+        if (n.C <= 8192) return go(Kern<layernorm_backward_rows_kernel<T, WT, 16, 16, 1, true>>(), 16);
+        return go(Kern<layernorm_backward_rows_kernel<T, WT, 32, 16, 1, false>>(), 32);
       }
     }
     return norm_width<VEC>(pieces, [&](auto nv, auto maxt) -> svdq_status {

@@ -101,64 +101,76 @@ __global__ void __launch_bounds__(MAXT, 1) int8_quantize_kernel(const Int8QuantA
   }
 }
 
-// Many rows of more than one warp: a block per row, rows streamed through the ring.
-template <typename T, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) int8_quantize_rows_kernel(const Int8QuantArgs a) {
-  constexpr int N = kVecN<T>, NV = kRowPieces<T>;
+// Many rows of more than one warp: a block per row, rows streamed through the
+// ring, the factors in registers, E elements a thread.
+template <typename T, int E, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W) int8_quantize_rows_kernel(const Int8QuantArgs a) {
+  constexpr int N = kVecN<T>, NV = E / N, H = N / 2;
   extern __shared__ __align__(16) unsigned char quant_ring[];
-  __shared__ float2 slots[2][32];
+  __shared__ float tops[2][W];
   __shared__ uint64_t full[kRingMaxStages];
-  const int warps = blockDim.x >> 5, tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int M = (int)a.M, step = (int)gridDim.x, ahead = a.depth * step;
+  const uint32_t row_bytes = (uint32_t)(a.K * (int)sizeof(T));
   RowRing<1> ring = {quant_ring, full, {static_cast<const unsigned char*>(a.x)}, {a.ldx * (long long)sizeof(T)},
-                     (uint32_t)(a.K * (int)sizeof(T)), a.depth};
+                     row_bytes, a.depth};
   if (tid == 0) ring.init();
+  if (tid < 2 * W) (&tops[0][0])[tid] = 0.f;
   __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
   if (tid == 0)
     for (int s = 0; s < a.depth; ++s) {
-      const long long m = blockIdx.x + (long long)s * gridDim.x;
-      if (m < a.M) ring.fetch(s, m);
+      const long long m = blockIdx.x + (long long)s * step;
+      if (m < M) ring.fetch(s, m);
     }
   bool in[NV];
-  float l[NV][N];
+  float2 l[NV][H];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int k = (v * (int)blockDim.x + tid) * N;
     in[v] = k < a.K;
-    if (a.mult && in[v]) {
-      load_params<float, N>(a.mult + k, l[v]);
-    } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) l[v][i] = 1.f;
-    }
+    for (int i = 0; i < H; ++i) l[v][i] = pair(1.f);
+    if (a.mult && in[v]) load_pairs<float, N>(a.mult + k, l[v]);
   }
   int stage = 0, turn = 0;
   uint32_t parity = 0;
-  for (long long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+  const unsigned char* piece = quant_ring + tid * 16;
+  int8_t* q = a.q + (long long)blockIdx.x * a.K + tid * N;
+  const long long q_step = (long long)step * a.K;
+  for (int m = blockIdx.x; m < M; m += step, turn ^= 1) {
     ring.wait(stage, parity);
-    float f[NV][N], amax = 0.f;
+    float2 f[NV][H];
+    float amax = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
       if (in[v]) {
-        unpack_vec<T>(*reinterpret_cast<const uint4*>(ring.row(stage, 0) + (v * (int)blockDim.x + tid) * 16), f[v]);
+        unpack_pairs<T>(*reinterpret_cast<const uint4*>(piece + v * (int)blockDim.x * 16), f[v]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          f[v][i] *= l[v][i];
-          amax = max_nan(amax, fabsf(f[v][i]));
+        for (int i = 0; i < H; ++i) {
+          f[v][i] = mul2_rn(f[v][i], l[v][i]);
+          amax = amax3_nan(amax, f[v][i].x, f[v][i].y);
         }
       }
-    amax = team_max_nan(amax, warps, slots[turn]);
-    if (tid == 0 && m + (long long)a.depth * gridDim.x < a.M) ring.fetch(stage, m + (long long)a.depth * gridDim.x);
+    amax = warp_amax_nan(amax);
+    if (lane == 0) tops[turn][warp] = amax;
+    __syncthreads();
+    if (tid == 0 && m < M - ahead) ring.fetch(stage, m + ahead);
+    piece += row_bytes;
     if (++stage == a.depth) {
       stage = 0;
       parity ^= 1u;
+      piece = quant_ring + tid * 16;
     }
+#pragma unroll
+    for (int i = 0; i < W; ++i) amax = max_nan(amax, tops[turn][i]);
     const Int8Scale sc = int8_scale(amax);
     if (tid == 0) a.s[m] = sc.s;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-      if (in[v]) int8_store<N>(a.q + m * a.K + (v * (int)blockDim.x + tid) * N, f[v], sc);
+      if (in[v]) int8_store<N>(q + v * (int)blockDim.x * N, f[v], sc);
+    q += q_step;
   }
 }
 

@@ -16,6 +16,8 @@
 
 #include <cstdint>
 
+#include "svdq_f32x2.cuh"
+
 namespace svdq {
 
 struct Int8Scale {
@@ -49,37 +51,58 @@ __device__ __forceinline__ float int8_code_small(float v, float s) {
   return (float)fmin(fmax(q, -127.0), 127.0);
 }
 
-// N consecutive codes (N = 1, 4 or 8; the address is a multiple of N).
+constexpr float kInt8Magic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer, left in the low bits
+
+// Candidate codes of two values, still carrying kInt8Magic; `far` collects how
+// far the quotients are from them.
+__device__ __forceinline__ float2 int8_quick(float2 v, const Int8Scale& sc, float& far) {
+  const float2 r = make_float2(sc.rcp, sc.rcp), magic = make_float2(kInt8Magic, kInt8Magic);
+  const float2 b = fma2_rn(v, r, magic);
+  const float2 d = fma2_rn(v, r, fma2_rn(b, make_float2(-1.f, -1.f), magic));
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(far) : "f"(far), "f"(d.x), "f"(d.y));
+  return b;
+}
+
+__device__ __forceinline__ float int8_careful(float v, float b, const Int8Scale& sc) {
+  if (sc.rcp == 0.f) return (sc.small ? int8_code_small(v, sc.s) : 0.f) + kInt8Magic;
+  return int8_settle(v, b - kInt8Magic, sc.s) + kInt8Magic;
+}
+
+// N = 4 or 8 consecutive codes (the address is a multiple of N).
 template <int N>
-__device__ __forceinline__ void int8_store(int8_t* out, const float (&v)[N], const Int8Scale& sc) {
-  constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer, left in the low bits
-  float b[N];
+__device__ __forceinline__ void int8_store(int8_t* out, const float2 (&v)[N / 2], const Int8Scale& sc) {
+  float2 b[N / 2];
   float far = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float t = v[i] * sc.rcp;
-    b[i] = t + kMagic;
-    far = fmaxf(far, fabsf(t - (b[i] - kMagic)));
-  }
-  if (sc.rcp == 0.f) {
+  for (int i = 0; i < N / 2; ++i) b[i] = int8_quick(v[i], sc, far);
+  if (far > 0.5f - 0x1p-15f || sc.rcp == 0.f) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) b[i] = (sc.small ? int8_code_small(v[i], sc.s) : 0.f) + kMagic;
-  } else if (far > 0.5f - 0x1p-15f) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) b[i] = int8_settle(v[i], b[i] - kMagic, sc.s) + kMagic;
+    for (int i = 0; i < N / 2; ++i) b[i] = make_float2(int8_careful(v[i].x, b[i].x, sc), int8_careful(v[i].y, b[i].y, sc));
   }
+  uint32_t w[N / 4];
+#pragma unroll
+  for (int j = 0; j < N / 4; ++j) {
+    const uint32_t lo = __byte_perm(__float_as_uint(b[2 * j].x), __float_as_uint(b[2 * j].y), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(b[2 * j + 1].x), __float_as_uint(b[2 * j + 1].y), 0x0040);
+    w[j] = __byte_perm(lo, hi, 0x5410);
+  }
+  if constexpr (N == 4) *reinterpret_cast<uint32_t*>(out) = w[0];
+  else *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+}
+
+// The same for an array of single values, N = 1 too.
+template <int N>
+__device__ __forceinline__ void int8_store(int8_t* out, const float (&v)[N], const Int8Scale& sc) {
   if constexpr (N == 1) {
-    out[0] = (int8_t)(__float_as_uint(b[0]) & 0xFFu);
+    float far = 0.f;
+    float b = int8_quick(make_float2(v[0], 0.f), sc, far).x;
+    if (far > 0.5f - 0x1p-15f || sc.rcp == 0.f) b = int8_careful(v[0], b, sc);
+    out[0] = (int8_t)(__float_as_uint(b) & 0xFFu);
   } else {
-    uint32_t w[N / 4];
+    float2 p[N / 2];
 #pragma unroll
-    for (int j = 0; j < N / 4; ++j) {
-      const uint32_t lo = __byte_perm(__float_as_uint(b[4 * j]), __float_as_uint(b[4 * j + 1]), 0x0040);
-      const uint32_t hi = __byte_perm(__float_as_uint(b[4 * j + 2]), __float_as_uint(b[4 * j + 3]), 0x0040);
-      w[j] = __byte_perm(lo, hi, 0x5410);
-    }
-    if constexpr (N == 4) *reinterpret_cast<uint32_t*>(out) = w[0];
-    else *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    for (int i = 0; i < N / 2; ++i) p[i] = make_float2(v[2 * i], v[2 * i + 1]);
+    int8_store<N>(out, p, sc);
   }
 }
 

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_kernel(const NormArgs a) {
         for (int i = 0; i < N; ++i) sq = fmaf(f[i] - mean, f[i] - mean, sq);
       }
     }
-    const float rstd = 1.f / sqrtf(team_sum(sq, warps, slots[1]) * inv_c + a.eps);
+    const float rstd = __frsqrt_rn(fmaf(team_sum(sq, warps, slots[1]), inv_c, a.eps));
     if (tid == 0) {
       if (a.mean) a.mean[m] = mean;
       if (a.rstd) a.rstd[m] = rstd;
@@ -155,25 +155,40 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_kernel(const NormArgs a) {
   }
 }
 
-// Forward for rows of more than one warp: a block per row, rows streamed through
-// the ring, weight and bias of the group kept in registers. Thread t holds the
-// pieces t, t + blockDim.x, ... of a row (kRowElems values).
+// What a warp leaves of a row: the sum, the sum of squares around the warp's
+// own mean, how many elements, the mean.
+__device__ __forceinline__ float4 warp_moments(float sum, float sq, float2 n) {
+  return make_float4(sum, sq, n.x, sum * n.y);
+}
+
+// Forward for rows of more than one warp, many of them: a block per row, rows
+// streamed through the ring, weight and bias of the group in registers. Thread
+// t holds the pieces t, t + blockDim.x, ... of a row, E elements: 32 of them
+// where the row has enough, so that what a row costs a thread besides its
+// elements (the wait, shuffles, the join) is shared by more. W: warps the block
+// may have; the join runs over all of them, unrolled (absent ones hold zeros).
 //
 // Mean and variance take one barrier: each warp forms its own mean and its own
-// sum of squares around that mean, and the block joins them,
+// sum of squares around that mean, and every thread joins the warps',
 //   M2 = sum_w (M2_w + n_w (mean_w - mean)^2).
-template <typename T, typename WT, int MAXT, bool QUANT>
-__global__ void __launch_bounds__(MAXT, 1) layernorm_rows_kernel(const NormArgs a) {
-  constexpr int N = kVecN<T>, NV = kRowPieces<T>;
+template <typename T, typename WT, int E, int W, bool QUANT>
+__global__ void __launch_bounds__(32 * W, 16 / W) layernorm_rows_kernel(const NormArgs a) {
+  constexpr int N = kVecN<T>, NV = E / N, H = N / 2;
   extern __shared__ __align__(16) unsigned char norm_ring[];
-  __shared__ float2 slots[2][32];
-  __shared__ float2 counts[32];                  // n_w and 1 / n_w
+  __shared__ float4 moments[2][W];
+  __shared__ float tops[2][W];
   __shared__ uint64_t full[kRingMaxStages];
-  const int warps = blockDim.x >> 5, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float inv_c = 1.f / (float)a.C;
+  const int M = (int)a.M, step = (int)gridDim.x;
+  const uint32_t row_bytes = (uint32_t)(a.C * (int)sizeof(T));
   RowRing<1> ring = {norm_ring, full, {static_cast<const unsigned char*>(a.x)}, {a.ldx * (long long)sizeof(T)},
-                     (uint32_t)(a.C * (int)sizeof(T)), a.depth};
+                     row_bytes, a.depth};
   if (tid == 0) ring.init();
+  if (tid < 2 * W) {
+    (&moments[0][0])[tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+    (&tops[0][0])[tid] = 0.f;
+  }
   bool in[NV];
   int mine = 0;
 #pragma unroll
@@ -182,69 +197,85 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_rows_kernel(const NormArgs 
     mine += in[v] ? N : 0;
   }
   mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-  if (lane == 0) counts[warp] = make_float2((float)mine, mine ? 1.f / (float)mine : 0.f);
+  const float n = (float)mine, inv_n = mine ? 1.f / (float)mine : 0.f;   // elements of this warp
   __syncthreads();
-  const float inv_n = counts[warp].y;
-  const float lane_n = lane < warps ? counts[lane].x : 0.f, lane_inv_n = lane < warps ? counts[lane].y : 0.f;
   grid_dependency_wait();
   grid_launch_dependents();
   if (tid == 0)
     for (int s = 0; s < a.depth; ++s) {
-      const long long m = blockIdx.x + (long long)s * gridDim.x;
-      if (m < a.M) ring.fetch(s, m);
+      const long long m = blockIdx.x + (long long)s * step;
+      if (m < M) ring.fetch(s, m);
     }
-  float w[NV][N], b[NV][N];
-  long long group = -1;
+  float2 w[NV][H], b[NV][H];
+  const int ahead = a.depth * step;
+  long long group_end = 0;                       // row at which the next group begins
   int stage = 0, turn = 0;
   uint32_t parity = 0;
-  for (long long m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
-    const long long g = (unsigned)m / (unsigned)a.rows_per_group;
-    if (g != group) {
-      group = g;
+  const unsigned char* piece = norm_ring + tid * 16;
+  T* y = static_cast<T*>(a.y) + blockIdx.x * a.ldy + tid * N;
+  for (int m = blockIdx.x; m < M; m += step, turn ^= 1) {
+    if (m >= group_end) {
+      const long long g = (unsigned)m / (unsigned)a.rows_per_group;
+      group_end = (g + 1) * a.rows_per_group;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int c = (v * (int)blockDim.x + tid) * N;
-        if (in[v]) {
-          norm_gain<WT, N>(a, g, c, w[v]);
-          if (a.b) load_params<WT, N>(static_cast<const WT*>(a.b) + g * a.C + c, b[v]);
-        }
-        if (!a.b) {
+        const long long c = g * a.C + (v * (int)blockDim.x + tid) * N;
 #pragma unroll
-          for (int i = 0; i < N; ++i) b[v][i] = 0.f;
+        for (int i = 0; i < H; ++i) {
+          w[v][i] = pair(1.f);
+          b[v][i] = pair(0.f);
         }
+        if (in[v] && a.w) {
+          load_pairs<WT, N>(static_cast<const WT*>(a.w) + c, w[v]);
+#pragma unroll
+          for (int i = 0; i < H; ++i) w[v][i] = add2_rn(w[v][i], pair(a.add));
+        }
+        if (in[v] && a.b) load_pairs<WT, N>(static_cast<const WT*>(a.b) + c, b[v]);
       }
     }
     ring.wait(stage, parity);
-    float f[NV][N], sum = 0.f;
+    float2 f[NV][H], sum2 = pair(0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const uint4 r = in[v] ? *reinterpret_cast<const uint4*>(ring.row(stage, 0) + (v * (int)blockDim.x + tid) * 16)
-                            : make_uint4(0, 0, 0, 0);
-      unpack_vec<T>(r, f[v]);
+      uint4 r = make_uint4(0, 0, 0, 0);
+      if (in[v]) r = *reinterpret_cast<const uint4*>(piece + v * (int)blockDim.x * 16);
+      unpack_pairs<T>(r, f[v]);
 #pragma unroll
-      for (int i = 0; i < N; ++i) sum += f[v][i];
+      for (int i = 0; i < H; ++i) sum2 = add2_rn(sum2, f[v][i]);
     }
-    sum = warp_sum(sum);
+    const float sum = warp_sum(sum2.x + sum2.y);
     const float own = sum * inv_n;
-    float sq = 0.f;
+    float2 sq2 = pair(0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
       if (in[v]) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) sq = fmaf(f[v][i] - own, f[v][i] - own, sq);
+        for (int i = 0; i < H; ++i) {
+          const float2 d = add2_rn(f[v][i], pair(-own));
+          sq2 = fma2_rn(d, d, sq2);
+        }
       }
-    sq = warp_sum(sq);
-    if (lane == 0) slots[turn][warp] = make_float2(sum, sq);
+    const float sq = warp_sum(sq2.x + sq2.y);
+    if (lane == 0) moments[turn][warp] = make_float4(sum, sq, n, own);
     __syncthreads();
-    if (tid == 0 && m + (long long)a.depth * gridDim.x < a.M) ring.fetch(stage, m + (long long)a.depth * gridDim.x);
-    const float2 t = lane < warps ? slots[turn][lane] : make_float2(0.f, 0.f);
-    const float mean = warp_sum(t.x) * inv_c;
-    const float d = t.x * lane_inv_n - mean;
-    const float rstd = 1.f / sqrtf(warp_sum(fmaf(lane_n * d, d, t.y)) * inv_c + a.eps);
+    if (tid == 0 && m < M - ahead) ring.fetch(stage, m + ahead);
+    piece += row_bytes;
     if (++stage == a.depth) {
       stage = 0;
       parity ^= 1u;
+      piece = norm_ring + tid * 16;
     }
+    float mean = 0.f, m2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) mean += moments[turn][i].x;
+    mean *= inv_c;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float4 t = moments[turn][i];
+      const float d = t.w - mean;
+      m2 += fmaf(t.z * d, d, t.y);
+    }
+    const float rstd = __frsqrt_rn(fmaf(m2, inv_c, a.eps));
     if (tid == 0) {
       if (a.mean) a.mean[m] = mean;
       if (a.rstd) a.rstd[m] = rstd;
@@ -252,33 +283,37 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_rows_kernel(const NormArgs 
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int i = 0; i < N; ++i) f[v][i] = fmaf((f[v][i] - mean) * rstd, w[v][i], b[v][i]);
+      for (int i = 0; i < H; ++i)
+        f[v][i] = fma2_rn(mul2_rn(add2_rn(f[v][i], pair(-mean)), pair(rstd)), w[v][i], b[v][i]);
     if constexpr (!QUANT) {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        if (in[v]) Piece<T, true>::store(static_cast<T*>(a.y) + m * a.ldy + (v * (int)blockDim.x + tid) * N, f[v]);
+        if (in[v]) *reinterpret_cast<uint4*>(y + v * (int)blockDim.x * N) = pack_pairs<T>(f[v]);
+      y += step * a.ldy;
     } else {
       float amax = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if (in[v]) {
           if (a.inv_lambda) {
-            float l[N];
-            load_params<float, N>(a.inv_lambda + (v * (int)blockDim.x + tid) * N, l);
+            float2 l[H];
+            load_pairs<float, N>(a.inv_lambda + (v * (int)blockDim.x + tid) * N, l);
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[v][i] *= l[i];
+            for (int i = 0; i < H; ++i) f[v][i] = mul2_rn(f[v][i], l[i]);
           }
 #pragma unroll
-          for (int i = 0; i < N; ++i) amax = max_nan(amax, fabsf(f[v][i]));
+          for (int i = 0; i < H; ++i) amax = amax3_nan(amax, f[v][i].x, f[v][i].y);
         }
-      __shared__ float2 tops[2][32];
-      const Int8Scale sc = int8_scale(team_max_nan(amax, warps, tops[turn]));
+      amax = warp_amax_nan(amax);
+      if (lane == 0) tops[turn][warp] = amax;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < W; ++i) amax = max_nan(amax, tops[turn][i]);
+      const Int8Scale sc = int8_scale(amax);
       if (tid == 0) a.s[m] = sc.s;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int c = (v * (int)blockDim.x + tid) * N;
-        if (in[v]) int8_store<N>(a.q + m * a.C + c, f[v], sc);
-      }
+      for (int v = 0; v < NV; ++v)
+        if (in[v]) int8_store<N>(a.q + (long long)m * a.C + (v * (int)blockDim.x + tid) * N, f[v], sc);
     }
   }
 }
@@ -418,42 +453,57 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormA
   }
 }
 
-// Backward for rows of more than one warp: as above with one team, the rows of
-// x and dy streamed through the ring.
-template <typename T, typename WT, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1) layernorm_backward_rows_kernel(const NormArgs a) {
-  constexpr int N = kVecN<T>, NV = kRowPieces<T>;
+// Backward for rows of more than one warp: a block per chunk of a group's rows,
+// rows of x and dy streamed through the ring, the chunk's dw and db in
+// registers (2 E of them), the weight in shared memory (each thread its own
+// columns: it is read back once a row, and its registers are worth more to a
+// second resident block). HOLD: xhat and h stay in registers between the row's
+// two sweeps; else (E = 32, rows of more than 8192) the second sweep forms them
+// again from the stage, which then waits for one more barrier.
+template <typename T, typename WT, int E, int W, int BLOCKS, bool HOLD>
+__global__ void __launch_bounds__(32 * W, BLOCKS) layernorm_backward_rows_kernel(const NormArgs a) {
+  constexpr int N = kVecN<T>, NV = E / N, H = N / 2;
   extern __shared__ __align__(16) unsigned char norm_ring[];
-  __shared__ float2 slots[2][32];
+  __shared__ __align__(16) float2 slots[2][W];
   __shared__ uint64_t full[kRingMaxStages];
-  const int warps = blockDim.x >> 5, tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const float inv_c = 1.f / (float)a.C;
+  const uint32_t row_bytes = (uint32_t)(a.C * (int)sizeof(T));
   RowRing<2> ring = {norm_ring, full,
                      {static_cast<const unsigned char*>(a.x), static_cast<const unsigned char*>(a.dy)},
-                     {a.ldx * (long long)sizeof(T), a.lddy * (long long)sizeof(T)},
-                     (uint32_t)(a.C * (int)sizeof(T)), a.depth};
+                     {a.ldx * (long long)sizeof(T), a.lddy * (long long)sizeof(T)}, row_bytes, a.depth};
+  float* gain = reinterpret_cast<float*>(norm_ring + 2 * (size_t)a.depth * row_bytes);   // [C]
   if (tid == 0) ring.init();
+  if (tid < 2 * W) (&slots[0][0])[tid] = pair(0.f);
   const long long g = blockIdx.x / a.chunks, groups = gridDim.x / a.chunks;
   const int chunk = (int)(blockIdx.x % a.chunks);
-  const long long row0 = g * a.rows_per_group, rows = min(a.rows_per_group, a.M - row0);
+  const long long row0 = g * a.rows_per_group;
+  const int rows = (int)min(a.rows_per_group, a.M - row0), ahead = a.depth * a.chunks;
   bool in[NV];
+  float2 dw[NV][H], db[NV][H];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) in[v] = (v * (int)blockDim.x + tid) * N < a.C;
+  for (int v = 0; v < NV; ++v) {
+    in[v] = (v * (int)blockDim.x + tid) * N < a.C;
+#pragma unroll
+    for (int i = 0; i < H; ++i) dw[v][i] = db[v][i] = pair(0.f);
+  }
   __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
   if (tid == 0)
     for (int s = 0; s < a.depth; ++s) {
-      const long long k = chunk + (long long)s * a.chunks;
+      const int k = chunk + s * a.chunks;
       if (k < rows) ring.fetch(s, row0 + k);
     }
-  float w[NV][N], dw[NV][N], db[NV][N];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    if (in[v]) norm_gain<WT, N>(a, g, (v * (int)blockDim.x + tid) * N, w[v]);
+  for (int v = 0; v < NV; ++v)
+    if (in[v]) {
+      const int c = (v * (int)blockDim.x + tid) * N;
+      float w[N];
+      norm_gain<WT, N>(a, g, c, w);
 #pragma unroll
-    for (int i = 0; i < N; ++i) dw[v][i] = db[v][i] = 0.f;
-  }
+      for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(gain + c + i) = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
   int stage = 0, turn = 0;
   uint32_t parity = 0;
   float mean = 0.f, rstd = 0.f;
@@ -461,42 +511,82 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_rows_kernel(const 
     mean = a.mean[row0 + chunk];
     rstd = a.rstd[row0 + chunk];
   }
-  for (long long k = chunk; k < rows; k += a.chunks, turn ^= 1) {
+  const unsigned char* at_x = norm_ring + tid * 16;
+  T* dx = static_cast<T*>(a.dx) + (row0 + chunk) * a.lddx + tid * N;
+  const long long dx_step = a.chunks * a.lddx;
+  const float* stat_mean = a.mean + row0;
+  const float* stat_rstd = a.rstd + row0;
+  for (int k = chunk; k < rows; k += a.chunks, turn ^= 1) {
     // the next row's statistics, ahead of their use
-    const long long next = min(k + a.chunks, rows - 1);
-    const float mean1 = a.mean[row0 + next], rstd1 = a.rstd[row0 + next];
+    const int next = min(k + a.chunks, rows - 1);
+    const float mean1 = stat_mean[next], rstd1 = stat_rstd[next];
     ring.wait(stage, parity);
-    float xh[NV][N], h[NV][N], s1 = 0.f, s2 = 0.f;
+    // xhat, dy and h = dy w of piece v
+    auto piece = [&](int v, float2 (&xh)[H], float2 (&dy)[H], float2 (&h)[H]) {
+      const unsigned char* at = at_x + v * (int)blockDim.x * 16;
+      unpack_pairs<T>(*reinterpret_cast<const uint4*>(at), xh);
+      unpack_pairs<T>(*reinterpret_cast<const uint4*>(at + row_bytes), dy);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (in[v]) {
-        unpack_vec<T>(*reinterpret_cast<const uint4*>(ring.row(stage, 0) + (v * (int)blockDim.x + tid) * 16), xh[v]);
-        unpack_vec<T>(*reinterpret_cast<const uint4*>(ring.row(stage, 1) + (v * (int)blockDim.x + tid) * 16), h[v]);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          xh[v][i] = (xh[v][i] - mean) * rstd;
-          dw[v][i] = fmaf(h[v][i], xh[v][i], dw[v][i]);
-          db[v][i] += h[v][i];
-          h[v][i] *= w[v][i];
-          s1 += h[v][i];
-          s2 = fmaf(h[v][i], xh[v][i], s2);
-        }
+      for (int i = 0; i < H; i += 2) {
+        const float4 w = *reinterpret_cast<const float4*>(gain + (v * (int)blockDim.x + tid) * N + 2 * i);
+        h[i] = mul2_rn(dy[i], make_float2(w.x, w.y));
+        h[i + 1] = mul2_rn(dy[i + 1], make_float2(w.z, w.w));
       }
-    }
-    const float2 s = team_sum2(s1, s2, warps, slots[turn]);
-    if (tid == 0 && k + (long long)a.depth * a.chunks < rows) ring.fetch(stage, row0 + k + (long long)a.depth * a.chunks);
-    if (++stage == a.depth) {
-      stage = 0;
-      parity ^= 1u;
-    }
-    const float m1 = s.x * inv_c, m2 = s.y * inv_c;
+#pragma unroll
+      for (int i = 0; i < H; ++i) xh[i] = mul2_rn(add2_rn(xh[i], pair(-mean)), pair(rstd));
+    };
+    float2 xh[HOLD ? NV : 1][H], h[HOLD ? NV : 1][H], s1 = pair(0.f), s2 = pair(0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
       if (in[v]) {
+        float2 dy[H];
+        constexpr bool K = HOLD;
+        float2(&x)[H] = xh[K ? v : 0], (&hh)[H] = h[K ? v : 0];
+        piece(v, x, dy, hh);
 #pragma unroll
-        for (int i = 0; i < N; ++i) h[v][i] = rstd * (h[v][i] - m1 - xh[v][i] * m2);
-        Piece<T, true>::store(static_cast<T*>(a.dx) + (row0 + k) * a.lddx + (v * (int)blockDim.x + tid) * N, h[v]);
+        for (int i = 0; i < H; ++i) {
+          dw[v][i] = fma2_rn(dy[i], x[i], dw[v][i]);
+          db[v][i] = add2_rn(db[v][i], dy[i]);
+          s1 = add2_rn(s1, hh[i]);
+          s2 = fma2_rn(hh[i], x[i], s2);
+        }
       }
+    const float s = warp_sum_halves(s1.x + s1.y, s2.x + s2.y, lane);
+    if ((lane & 15) == 0) reinterpret_cast<float*>(&slots[turn][tid >> 5])[lane >> 4] = s;
+    __syncthreads();
+    if (HOLD && tid == 0 && k + ahead < rows) ring.fetch(stage, row0 + k + ahead);
+    float2 t = pair(0.f);
+#pragma unroll
+    for (int i = 0; i < W; i += 2) {
+      const float4 u = *reinterpret_cast<const float4*>(&slots[turn][i]);
+      t = add2_rn(t, add2_rn(make_float2(u.x, u.y), make_float2(u.z, u.w)));
+    }
+    // dx = rstd h - rstd m1 - xhat rstd m2
+    const float2 r1 = pair(-rstd * (t.x * inv_c)), r2 = pair(-rstd * (t.y * inv_c));
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (in[v]) {
+        constexpr bool K = HOLD;
+        float2(&x)[H] = xh[K ? v : 0], (&hh)[H] = h[K ? v : 0];
+        if constexpr (!HOLD) {
+          float2 dy[H];
+          piece(v, x, dy, hh);
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) hh[i] = fma2_rn(x[i], r2, fma2_rn(hh[i], pair(rstd), r1));
+        *reinterpret_cast<uint4*>(dx + v * (int)blockDim.x * N) = pack_pairs<T>(hh);
+      }
+    if (!HOLD) {
+      __syncthreads();
+      if (tid == 0 && k + ahead < rows) ring.fetch(stage, row0 + k + ahead);
+    }
+    dx += dx_step;
+    at_x += 2 * row_bytes;
+    if (++stage == a.depth) {
+      stage = 0;
+      parity ^= 1u;
+      at_x = norm_ring + tid * 16;
+    }
     mean = mean1;
     rstd = rstd1;
   }
@@ -509,9 +599,9 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_rows_kernel(const 
     if (in[v]) {
       const long long c = g * a.C + (v * (int)blockDim.x + tid) * N;
 #pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        if (pw) *reinterpret_cast<float4*>(pw + c + i) = make_float4(dw[v][i], dw[v][i + 1], dw[v][i + 2], dw[v][i + 3]);
-        if (pb) *reinterpret_cast<float4*>(pb + c + i) = make_float4(db[v][i], db[v][i + 1], db[v][i + 2], db[v][i + 3]);
+      for (int i = 0; i < H; i += 2) {
+        if (pw) *reinterpret_cast<float4*>(pw + c + 2 * i) = make_float4(dw[v][i].x, dw[v][i].y, dw[v][i + 1].x, dw[v][i + 1].y);
+        if (pb) *reinterpret_cast<float4*>(pb + c + 2 * i) = make_float4(db[v][i].x, db[v][i].y, db[v][i + 1].x, db[v][i + 1].y);
       }
     }
 }
@@ -528,8 +618,10 @@ __global__ void __launch_bounds__(256) layernorm_partials_kernel(const float* __
   grid_dependency_wait();
   grid_launch_dependents();
   float s = 0.f;
-  if (c < cols)
+  if (c < cols) {
+#pragma unroll 8
     for (int k = w; k < chunks; k += 8) s += part[(2ll * k + which) * cols + c];
+  }
   sums[w][lane] = s;
   __syncthreads();
   float* out = which ? db : dw;

@@ -13,19 +13,24 @@
 // then sincospif works on a value in [-1, 1].
 //
 // Bound: HBM, 2 bytes read and 2 written per 16-bit element and nothing reused
-// but the angles. A block takes one token at a time (or a share of its heads
-// when tokens are few): its threads first fill a table of R/2 (cos, sin) in
-// shared memory, once for all heads, then stream the heads, 16 bytes of each
-// operand per thread.
+// but the angles. A block takes a few tokens (or a share of one token's heads
+// when tokens are few): its threads first fill a table of (cos, sin) in shared
+// memory, once for all heads, then stream the heads. A thread keeps one 16-byte
+// place of the head with that place's cosines in registers and walks the heads,
+// four loads in flight, with nothing to divide or look up per head.
 #pragma once
 
+#include "svdq_f32x2.cuh"
 #include "svdq_ptx.cuh"
+#include "svdq_rows.cuh"
 #include "svdq_vec.cuh"
 
 namespace svdq {
 
 constexpr int kRopeMaxAxes = 8;
 constexpr int kRopeMaxD = 512;
+constexpr int kRopeTable = 512;    // (cos, sin) of a block's tokens
+constexpr int kRopeThreads = 256;
 
 struct RopeArgs {
   const void* x;
@@ -34,7 +39,7 @@ struct RopeArgs {
   const void* pos;               // [pos_rows][axes], int32 or fp32
   const double* freq;            // [R/2]
   long long T, pos_rows;
-  int heads, heads_per_block, D, R, axes;
+  int heads, heads_per_block, tokens_per_block, D, R, axes;
   int axis_end[kRopeMaxAxes];    // last pair + 1 of each axis
   int pos_fp32, inverse;
 };
@@ -49,86 +54,140 @@ __device__ __forceinline__ double rope_position(const RopeArgs& a, long long p, 
 }
 
 
-// N values at p as fp32 and back: one 16-byte vector, or one value.
-template <typename T, int N>
-__device__ __forceinline__ void rope_load(const T* p, float (&f)[N]) {
-  if constexpr (N == 1) f[0] = to_float(*p);
-  else unpack_vec<T>(load_once(p), f);
-}
-
-template <typename T, int N>
-__device__ __forceinline__ void rope_store(T* p, const float (&f)[N]) {
-  if constexpr (N == 1) *p = from_float<T>(f[0]);
-  else *reinterpret_cast<uint4*>(p) = pack_vec<T>(f);
-}
+// A place of the head: what a thread loads, turns and stores of it.
+// Interleaved pairs: one piece of V values, V / 2 pairs; halves: V values of
+// each half, V pairs. The paired fp32 instructions fit halves (two pairs' first
+// elements beside each other); interleaved pairs would have to be swapped for
+// them, which costs what they save.
+template <typename T, bool HALVES, bool VEC>
+struct RopePlace {
+  static constexpr int V = VEC ? kVecN<T> : HALVES ? 1 : 2;
+  static constexpr int kPairs = HALVES ? V : V / 2;
+  struct Raw {
+    uint4 a, b;
+    T s, t;
+  };
+  struct Turn {
+    float c[kPairs], s[kPairs];
+  };
+  __device__ static void load(Raw& r, const T* p, int half) {
+    if constexpr (VEC) {
+      r.a = load_once(p);
+      if constexpr (HALVES) r.b = load_once(p + half);
+    } else {
+      r.s = p[0];
+      r.t = p[HALVES ? half : 1];
+    }
+  }
+  __device__ static void turn(const Raw& r, const Turn& w, T* p, int half) {
+    if constexpr (!VEC) {
+      const float a = to_float(r.s), b = to_float(r.t);
+      p[0] = from_float<T>(fmaf(-b, w.s[0], a * w.c[0]));
+      p[HALVES ? half : 1] = from_float<T>(fmaf(a, w.s[0], b * w.c[0]));
+    } else if constexpr (!HALVES) {
+      float f[V], o[V];
+      unpack_vec<T>(r.a, f);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        o[2 * i] = fmaf(-f[2 * i + 1], w.s[i], f[2 * i] * w.c[i]);
+        o[2 * i + 1] = fmaf(f[2 * i], w.s[i], f[2 * i + 1] * w.c[i]);
+      }
+      *reinterpret_cast<uint4*>(p) = pack_vec<T>(o);
+    } else {
+      float2 a[V / 2], b[V / 2], o[V / 2];
+      unpack_pairs<T>(r.a, a);
+      unpack_pairs<T>(r.b, b);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i)
+        o[i] = fma2_rn(b[i], make_float2(-w.s[2 * i], -w.s[2 * i + 1]),
+                       mul2_rn(a[i], make_float2(w.c[2 * i], w.c[2 * i + 1])));
+      *reinterpret_cast<uint4*>(p) = pack_pairs<T>(o);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i)
+        o[i] = fma2_rn(a[i], make_float2(w.s[2 * i], w.s[2 * i + 1]),
+                       mul2_rn(b[i], make_float2(w.c[2 * i], w.c[2 * i + 1])));
+      *reinterpret_cast<uint4*>(p + half) = pack_pairs<T>(o);
+    }
+  }
+};
 
 // HALVES: pairs (i, i + R/2), else (2i, 2i+1). VEC: 16-byte pieces (every
 // address, stride and section boundary is a multiple of 16 bytes), else one
 // pair per thread.
 template <typename T, bool HALVES, bool VEC>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeArgs a) {
-  __shared__ float2 cs[kRopeMaxD / 2];
-  constexpr int V = VEC ? kVecN<T> : 1;
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+  using Place = RopePlace<T, HALVES, VEC>;
+  constexpr int NP = Place::kPairs;
+  constexpr int kHeads = HALVES ? 2 : 4;   // in flight per thread: four loads
+  __shared__ __align__(16) float2 cs[kRopeTable];
   const int half = a.R / 2;
-  grid_dependency_wait();
-  grid_launch_dependents();
   const int h0 = blockIdx.y * a.heads_per_block;
   const int nh = min(a.heads_per_block, a.heads - h0);
-  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const long long p = t % a.pos_rows;
-    for (int i = threadIdx.x; i < half; i += blockDim.x) {
-      // angle in half turns, reduced to [-1, 1]
-      double turn = rope_position(a, p, i) * a.freq[i] * 0.31830988618379067154;
-      turn -= 2.0 * rint(0.5 * turn);
-      float s, c;
-      sincospif((float)turn, &s, &c);
-      cs[i] = make_float2(c, a.inverse ? -s : s);
+  const long long t0 = (long long)blockIdx.x * a.tokens_per_block;
+  const int nt = (int)min((long long)a.tokens_per_block, a.T - t0);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int j = threadIdx.x; j < nt * half; j += blockDim.x) {
+    const int i = j % half;
+    // angle in half turns, reduced to [-1, 1]
+    double turn = rope_position(a, (t0 + j / half) % a.pos_rows, i) * a.freq[i] * 0.31830988618379067154;
+    turn -= 2.0 * rint(0.5 * turn);
+    float s, c;
+    sincospif((float)turn, &s, &c);
+    cs[j] = make_float2(c, a.inverse ? -s : s);
+  }
+  __syncthreads();
+  // places of a head that turn, then 16-byte (or single) pieces that do not
+  const int turned = half / NP;
+  constexpr int kCopy = VEC ? kVecN<T> : 1;
+  const int items = turned + (a.D - a.R) / kCopy;
+  const int per_pass = max(1, (int)blockDim.x / items);       // heads a pass of the block covers
+  const int first = (int)threadIdx.x / items;
+  if (first >= per_pass) return;
+  const int passes = first < nh ? (nh - first + per_pass - 1) / per_pass : 0;
+  const long long x_step = per_pass * a.xh, y_step = per_pass * a.yh;
+  const T* x0 = static_cast<const T*>(a.x) + t0 * a.xt + (h0 + first) * a.xh;
+  T* y0 = static_cast<T*>(a.y) + t0 * a.yt + (h0 + first) * a.yh;
+  for (int item = (int)threadIdx.x - first * items; item < items; item += blockDim.x) {
+    if (item >= turned) {
+      const int at = a.R + (item - turned) * kCopy;
+      for (int k = 0; k < nt; ++k) {
+        const T* x = x0 + k * a.xt + at;
+        T* y = y0 + k * a.yt + at;
+        for (int j = 0; j < passes; ++j, x += x_step, y += y_step) {
+          if constexpr (VEC) *reinterpret_cast<uint4*>(y) = load_once(x);
+          else *y = *x;
+        }
+      }
+      continue;
     }
-    __syncthreads();
-    const T* x = static_cast<const T*>(a.x) + t * a.xt + h0 * a.xh;
-    T* y = static_cast<T*>(a.y) + t * a.yt + h0 * a.yh;
-    // items of a head: pieces of pairs, then pieces of what passes unchanged
-    const int turned = HALVES ? half / V : (VEC ? a.R / V : half);
-    const int items = turned + (a.D - a.R) / V;
-    for (int j = threadIdx.x; j < nh * items; j += blockDim.x) {
-      const int h = j / items, i = j - h * items;
-      const T* xr = x + h * a.xh;
-      T* yr = y + h * a.yh;
-      if (i >= turned) {
-        float f[V];
-        const int e = a.R + (i - turned) * V;
-        rope_load<T, V>(xr + e, f);
-        rope_store<T, V>(yr + e, f);
-      } else if constexpr (HALVES) {
-        float u[V], v[V], p0[V], p1[V];
-        rope_load<T, V>(xr + i * V, u);
-        rope_load<T, V>(xr + half + i * V, v);
+    const int at = HALVES ? item * NP : 2 * item * NP;
+    for (int k = 0; k < nt; ++k) {
+      const T* x = x0 + k * a.xt + at;
+      T* y = y0 + k * a.yt + at;
+      typename Place::Turn w;
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const float2 w = cs[i * V + k];
-          p0[k] = u[k] * w.x - v[k] * w.y;
-          p1[k] = v[k] * w.x + u[k] * w.y;
-        }
-        rope_store<T, V>(yr + i * V, p0);
-        rope_store<T, V>(yr + half + i * V, p1);
-      } else if constexpr (VEC) {
-        float u[V], o[V];
-        rope_load<T, V>(xr + i * V, u);
+      for (int i = 0; i < NP; ++i) {
+        const float2 t = cs[k * half + item * NP + i];
+        w.c[i] = t.x;
+        w.s[i] = t.y;
+      }
+      for (int j = passes; j > 0; j -= kHeads) {
+        typename Place::Raw r[kHeads];
 #pragma unroll
-        for (int k = 0; k < V; k += 2) {
-          const float2 w = cs[(i * V + k) / 2];
-          o[k] = u[k] * w.x - u[k + 1] * w.y;
-          o[k + 1] = u[k + 1] * w.x + u[k] * w.y;
-        }
-        rope_store<T, V>(yr + i * V, o);
-      } else {
-        const float u = to_float(xr[2 * i]), v = to_float(xr[2 * i + 1]);
-        const float2 w = cs[i];
-        yr[2 * i] = from_float<T>(u * w.x - v * w.y);
-        yr[2 * i + 1] = from_float<T>(v * w.x + u * w.y);
+        for (int u = 0; u < kHeads; ++u)
+          if (u < j) {
+            Place::load(r[u], x, half);
+            x += x_step;
+          }
+#pragma unroll
+        for (int u = 0; u < kHeads; ++u)
+          if (u < j) {
+            Place::turn(r[u], w, y, half);
+            y += y_step;
+          }
       }
     }
-    __syncthreads();
   }
 }
 

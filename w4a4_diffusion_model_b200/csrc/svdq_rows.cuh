@@ -8,6 +8,7 @@
 // the thread that issues the copies refills the stage behind that barrier.
 #pragma once
 
+#include "svdq_f32x2.cuh"
 #include "svdq_ptx.cuh"
 #include "svdq_vec.cuh"
 
@@ -47,9 +48,59 @@ struct RowRing {
   }
 };
 
-// Elements a thread holds of a row in these kernels, and the pieces they are.
-constexpr int kRowElems = 16;
+// A 16-byte piece as pairs of fp32, and back.
 template <typename T>
-inline constexpr int kRowPieces = kRowElems / kVecN<T>;
+__device__ __forceinline__ void unpack_pairs(const uint4& r, float2 (&f)[kVecN<T> / 2]) {
+  float t[kVecN<T>];
+  unpack_vec<T>(r, t);
+#pragma unroll
+  for (int i = 0; i < kVecN<T> / 2; ++i) f[i] = make_float2(t[2 * i], t[2 * i + 1]);
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack_pairs(const float2 (&f)[kVecN<T> / 2]) {
+  float t[kVecN<T>];
+#pragma unroll
+  for (int i = 0; i < kVecN<T> / 2; ++i) {
+    t[2 * i] = f[i].x;
+    t[2 * i + 1] = f[i].y;
+  }
+  return pack_vec<T>(t);
+}
+
+template <typename WT, int N>
+__device__ __forceinline__ void load_pairs(const WT* p, float2 (&f)[N / 2]) {
+  float t[N];
+  load_params<WT, N>(p, t);
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) f[i] = make_float2(t[2 * i], t[2 * i + 1]);
+}
+
+__device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+
+// Sums of a and b over a warp in six shuffles: the half-warps take one each.
+// Lanes 0-15 end with the sum of a, lanes 16-31 with the sum of b.
+__device__ __forceinline__ float warp_sum_halves(float a, float b, int lane) {
+  const bool hi = (lane & 16) != 0;
+  float v = hi ? b : a;
+  v += __shfl_xor_sync(0xFFFFFFFFu, hi ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// The largest |v| of a warp, NaN if any is.
+__device__ __forceinline__ float warp_amax_nan(float v) {
+  float r;
+  asm("redux.sync.max.abs.NaN.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// max(|a|, |b|, |c|), NaN if any is.
+__device__ __forceinline__ float amax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 }  // namespace svdq
