@@ -164,7 +164,7 @@ svdq_status launch_int8_gemm(const svdq::Int8GemmArgs& args, const void* Qx, con
   static std::atomic<int> done[kMaxDevices];
   cudaError_t err = cudaSuccess;
   per_device_once(done, current_device(), [&err, kern] {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes(C::kMany));
     return err == cudaSuccess ? 1 : 0;
   });
   if (err != cudaSuccess)
@@ -182,8 +182,9 @@ svdq_status launch_int8_gemm(const svdq::Int8GemmArgs& args, const void* Qx, con
   const int64_t tiles = (int64_t)((a.N + NB - 1) / NB) * ((a.M + 127) / 128);
   if (tiles > (1ll << 31) - 1) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "too many tiles");
   cudaLaunchAttribute attr[2];
+  a.stages = tiles * splits <= sm_count() ? C::kMany : C::kFew;
   cudaLaunchConfig_t cfg =
-      pdl_config(dim3((unsigned)tiles, 1, (unsigned)splits), svdq::kI8Threads, C::kBytes, st, attr);
+      pdl_config(dim3((unsigned)tiles, 1, (unsigned)splits), svdq::kI8Threads, C::bytes(a.stages), st, attr);
   if (splits > 1) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 1;
@@ -195,8 +196,9 @@ svdq_status launch_int8_gemm(const svdq::Int8GemmArgs& args, const void* Qx, con
   return SVDQ_OK;
 }
 
+template <int NB>
 cudaLaunchConfig_t int8_pair_config(int clusters, cudaStream_t st, cudaLaunchAttribute* attr) {
-  cudaLaunchConfig_t cfg = pdl_config(2 * clusters, svdq::kP8Threads, svdq::kP8Bytes, st, attr);
+  cudaLaunchConfig_t cfg = pdl_config(2 * clusters, svdq::kP8Threads, svdq::Int8PairCfg<NB>::kBytes, st, attr);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 2;
   attr[1].val.clusterDim.y = 1;
@@ -207,17 +209,17 @@ cudaLaunchConfig_t int8_pair_config(int clusters, cudaStream_t st, cudaLaunchAtt
 
 // Clusters of the pair kernel that fit on the device at once (0: none); also
 // sets the kernel's shared-memory attribute there.
-template <typename OT>
+template <int NB, typename OT>
 int int8_pair_clusters() {
   static std::atomic<int> cache[kMaxDevices];
   return per_device_once(cache, current_device(), [] {
-    auto kern = svdq::svdq_int8_gemm_pair_kernel<OT>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, svdq::kP8Bytes) != cudaSuccess) {
+    auto kern = svdq::svdq_int8_gemm_pair_kernel<NB, OT>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, svdq::Int8PairCfg<NB>::kBytes) != cudaSuccess) {
       cudaGetLastError();
       return 0;
     }
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = int8_pair_config(sm_count() / 2, nullptr, attr);
+    cudaLaunchConfig_t cfg = int8_pair_config<NB>(sm_count() / 2, nullptr, attr);
     std::swap(attr[0], attr[1]);
     cfg.numAttrs = 1;
     int n = 0;
@@ -229,7 +231,7 @@ int int8_pair_clusters() {
   }) - 1;
 }
 
-template <typename OT>
+template <int NB, typename OT>
 svdq_status launch_int8_pair(const svdq::Int8GemmArgs& a, const void* Qx, const void* Qw, int clusters,
                              cudaStream_t st) {
   CUtensorMap tx, tw, ty;
@@ -237,7 +239,7 @@ svdq_status launch_int8_pair(const svdq::Int8GemmArgs& a, const void* Qx, const 
   if ((r = make_tmap(&tx, Qx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.M, svdq::kI8KTile, 128,
                      CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
     return r;
-  if ((r = make_tmap(&tw, Qw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N, svdq::kI8KTile, 128,
+  if ((r = make_tmap(&tw, Qw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N, svdq::kI8KTile, NB / 2,
                      CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
     return r;
   const uint64_t ld = a.M > 1 ? (uint64_t)a.ldy : (uint64_t)a.N;
@@ -246,19 +248,42 @@ svdq_status launch_int8_pair(const svdq::Int8GemmArgs& a, const void* Qx, const 
   if (tma_y && (r = make_tmap(&ty, a.y, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.N * sizeof(OT), (uint64_t)a.M,
                               128, 32, CU_TENSOR_MAP_SWIZZLE_128B, ld * sizeof(OT))) != SVDQ_OK)
     return r;
-  const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+  const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + NB - 1) / NB);
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = int8_pair_config((int)std::min<int64_t>(tiles, clusters), st, attr);
-  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::svdq_int8_gemm_pair_kernel<OT>, tx, tw, ty, a, tma_y ? 1 : 0));
+  cudaLaunchConfig_t cfg = int8_pair_config<NB>((int)std::min<int64_t>(tiles, clusters), st, attr);
+  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::svdq_int8_gemm_pair_kernel<NB, OT>, tx, tw, ty, a, tma_y ? 1 : 0));
   return SVDQ_OK;
 }
 
+template <int MT, typename OT>
+svdq_status launch_int8_few(const svdq::Int8GemmArgs& a, const void* Qx, const void* Qw, cudaStream_t st) {
+  const int warps = svdq::kGvThreads / 32;
+  int warps_k = 1;
+  while (warps_k < warps && warps_k * 512 < a.K) warps_k *= 2;
+  const int channels = svdq::kGvChannels * (warps / warps_k);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = pdl_config((a.N + channels - 1) / channels, svdq::kGvThreads, 0, st, attr);
+  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::int8_few_tokens_kernel<MT, OT>, static_cast<const int8_t*>(Qx),
+                               static_cast<const int8_t*>(Qw), a, warps_k));
+  return SVDQ_OK;
+}
+
+// Which kernel and split serves a product (environment override for sweeps).
 template <typename OT>
 svdq_status launch_int8_linear(const svdq::Int8GemmArgs& a, const void* Qx, const void* Qw, cudaStream_t st) {
-  const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
-  const int clusters = tiles >= 37 && tiles < (1ll << 31) ? int8_pair_clusters<OT>() : 0;
-  if (clusters > 0) return launch_int8_pair<OT>(a, Qx, Qw, clusters, st);
-  return launch_int8_gemm<128, OT>(a, Qx, Qw, 1, st);
+  const char* f = getenv("SVDQ_I8");
+  int mode = f ? atoi(f) : 0;      // 1: pair, 2: few, 1xxs: NB=64 splits s, 2xxs: NB=128
+  if (mode == 0) mode = a.M <= 8 ? 2 : (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256) >= 37 ? 1 : 201;
+  if (mode == 1) return launch_int8_pair<256, OT>(a, Qx, Qw, int8_pair_clusters<256, OT>(), st);
+  if (mode == 3) return launch_int8_pair<128, OT>(a, Qx, Qw, int8_pair_clusters<128, OT>(), st);
+  if (mode == 2) {
+    if (a.M == 1) return launch_int8_few<1, OT>(a, Qx, Qw, st);
+    if (a.M == 2) return launch_int8_few<2, OT>(a, Qx, Qw, st);
+    if (a.M <= 4) return launch_int8_few<4, OT>(a, Qx, Qw, st);
+    return launch_int8_few<8, OT>(a, Qx, Qw, st);
+  }
+  if (mode / 100 == 1) return launch_int8_gemm<64, OT>(a, Qx, Qw, mode % 100, st);
+  return launch_int8_gemm<128, OT>(a, Qx, Qw, mode % 100, st);
 }
 
 // ---------------------------------------------------------------- norm
@@ -377,14 +402,15 @@ svdq_status launch_rope(svdq::RopeArgs a, bool halves, cudaStream_t st) {
   bool vec = (a.D - a.R) % V == 0 && (halves ? a.R / 2 : a.R) % V == 0 && a.D % V == 0;
   if (a.T > 1) vec = vec && a.xt % V == 0 && a.yt % V == 0;
   if (a.heads > 1) vec = vec && a.xh % V == 0 && a.yh % V == 0;
-  // Enough blocks for every SM come first: few tokens share their heads among
-  // several blocks, many go together so that their angles fill the block.
-  const int64_t want = 8ll * sm_count();
-  const int shares = (int)std::min<int64_t>(a.heads, std::max<int64_t>(1, want / a.T));
+  // Two waves of resident blocks (4 per SM) at the least: few tokens share their
+  // heads among several blocks, many go together, as far as the angle table
+  // holds them. 4608 x 48 heads: 22.7, 22.5 and 23.5 us with 4, 8 and 16 per SM.
+  const int64_t resident = 8ll * sm_count(), T64 = a.T;
+  const int shares = (int)std::min<int64_t>(a.heads, std::max<int64_t>(1, resident / T64));
   a.heads_per_block = (a.heads + shares - 1) / shares;
   a.tokens_per_block = (int)std::max<int64_t>(
-      1, std::min<int64_t>({a.T / want, (int64_t)svdq::kRopeTable / (a.R / 2), (int64_t)svdq::kRopeThreads / (a.R / 2)}));
-  const dim3 grid((unsigned)((a.T + a.tokens_per_block - 1) / a.tokens_per_block),
+      1, std::min<int64_t>((T64 + resident - 1) / resident, (int64_t)svdq::kRopeTable / (a.R / 2)));
+  const dim3 grid((unsigned)((T64 + a.tokens_per_block - 1) / a.tokens_per_block),
                   (unsigned)((a.heads + a.heads_per_block - 1) / a.heads_per_block));
   const int items = a.heads_per_block * (vec ? (a.R / (halves ? 2 * V : V) + (a.D - a.R) / V) : a.D - a.R / 2);
   const int threads = std::min(svdq::kRopeThreads, round_up(std::max(items, a.R / 2), 32));
@@ -433,7 +459,7 @@ svdq_status svdq_int8_linear(int64_t M, int64_t K, int64_t N, const void* Qx, co
   if ((r = check_rows("Y", M, N, ldy)) != SVDQ_OK) return r;
   if ((r = check_device()) != SVDQ_OK) return r;
   if (M == 0) return SVDQ_OK;
-  const svdq::Int8GemmArgs a{Sx, Sw, bias, Y, ldy, (int)M, (int)N, (int)K, 0};
+  const svdq::Int8GemmArgs a{Sx, Sw, bias, Y, ldy, (int)M, (int)N, (int)K, 0, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return with_type(y_dtype, [&](auto tag) -> svdq_status {
     using T = typename decltype(tag)::type;
@@ -595,6 +621,7 @@ svdq_status svdq_rope(int64_t T, int32_t heads, int32_t D, int dtype, const void
     R += axis_dims[i];
     a.axis_end[i] = (int)(R / 2);
   }
+  for (int i = axes; i < svdq::kRopeMaxAxes; ++i) a.axis_end[i] = svdq::kRopeMaxD;
   if (R > D) return fail(SVDQ_ERR_INVALID_ARG, "the axes have %lld elements, a head has %d", (long long)R, (int)D);
   const bool any = T > 0 && heads > 0;
   if (any && (!X || !Y || !positions || !freqs)) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
@@ -611,7 +638,7 @@ svdq_status svdq_rope(int64_t T, int32_t heads, int32_t D, int dtype, const void
   if ((r = check_device()) != SVDQ_OK) return r;
   if (!any) return SVDQ_OK;
   a.x = X; a.y = Y; a.xt = x_token_stride; a.xh = x_head_stride; a.yt = y_token_stride; a.yh = y_head_stride;
-  a.pos = positions; a.freq = freqs; a.T = T; a.pos_rows = pos_rows; a.heads = heads; a.D = D; a.R = (int)R;
+  a.pos = positions; a.freq = freqs; a.T = (int)T; a.pos_rows = (int)pos_rows; a.heads = heads; a.D = D; a.R = (int)R;
   a.axes = axes; a.pos_fp32 = pos_dtype == SVDQ_FP32; a.inverse = (flags & SVDQ_ROPE_INVERSE) != 0;
   return with_type(dtype, [&](auto tag) -> svdq_status {
     using E = typename decltype(tag)::type;

@@ -16,8 +16,8 @@
 // but the angles. A block takes a few tokens (or a share of one token's heads
 // when tokens are few): its threads first fill a table of (cos, sin) in shared
 // memory, once for all heads, then stream the heads. A thread keeps one 16-byte
-// place of the head with that place's cosines in registers and walks the heads,
-// four loads in flight, with nothing to divide or look up per head.
+// place of the head and walks the (token, head) rows, the next rows' loads always
+// ahead of the present rows' arithmetic, the first ones ahead of the angles.
 #pragma once
 
 #include "svdq_f32x2.cuh"
@@ -38,21 +38,20 @@ struct RopeArgs {
   long long xt, xh, yt, yh;      // token and head strides, in elements
   const void* pos;               // [pos_rows][axes], int32 or fp32
   const double* freq;            // [R/2]
-  long long T, pos_rows;
+  int T, pos_rows;
   int heads, heads_per_block, tokens_per_block, D, R, axes;
-  int axis_end[kRopeMaxAxes];    // last pair + 1 of each axis
+  int axis_end[kRopeMaxAxes];    // last pair + 1 of each axis; past every pair where there is no axis
   int pos_fp32, inverse;
 };
 
-// Position of token row `p` on the axis of pair i.
-__device__ __forceinline__ double rope_position(const RopeArgs& a, long long p, int i) {
+// Position of row `p` on the axis of pair i.
+__device__ __forceinline__ double rope_position(const RopeArgs& a, unsigned p, int i) {
   int axis = 0;
 #pragma unroll
-  for (int k = 0; k < kRopeMaxAxes - 1; ++k) axis += (k < a.axes - 1 && i >= a.axis_end[k]) ? 1 : 0;
-  const long long at = p * a.axes + axis;
+  for (int k = 0; k < kRopeMaxAxes - 1; ++k) axis += i >= a.axis_end[k] ? 1 : 0;
+  const size_t at = (size_t)p * a.axes + axis;
   return a.pos_fp32 ? (double)static_cast<const float*>(a.pos)[at] : (double)static_cast<const int*>(a.pos)[at];
 }
-
 
 // A place of the head: what a thread loads, turns and stores of it.
 // Interleaved pairs: one piece of V values, V / 2 pairs; halves: V values of
@@ -111,81 +110,127 @@ struct RopePlace {
   }
 };
 
+// Walks the rows (token, head) of a block in steps of `per_pass` heads.
+template <typename P>
+struct RopeCursor {
+  P* p;
+  int k, h;                      // token and head within the block
+  long long step, wrap;          // elements per step, and from a token's heads to the next token's
+  __device__ void next(int per_pass, int nh) {
+    p += step;
+    h += per_pass;
+    while (h >= nh) {
+      h -= nh;
+      ++k;
+      p += wrap;
+    }
+  }
+};
+
 // HALVES: pairs (i, i + R/2), else (2i, 2i+1). VEC: 16-byte pieces (every
 // address, stride and section boundary is a multiple of 16 bytes), else one
 // pair per thread.
 template <typename T, bool HALVES, bool VEC>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, HALVES ? 3 : 4) rope_kernel(const RopeArgs a) {
   using Place = RopePlace<T, HALVES, VEC>;
   constexpr int NP = Place::kPairs;
-  constexpr int kHeads = HALVES ? 2 : 4;   // in flight per thread: four loads
-  __shared__ __align__(16) float2 cs[kRopeTable];
+  constexpr int kRows = HALVES ? 1 : 2;   // loaded at a time (two loads; twice as many measured no faster)
+  __shared__ __align__(16) float table[2][kRopeTable];   // cos and sin, [token][pair]
   const int half = a.R / 2;
   const int h0 = blockIdx.y * a.heads_per_block;
   const int nh = min(a.heads_per_block, a.heads - h0);
-  const long long t0 = (long long)blockIdx.x * a.tokens_per_block;
-  const int nt = (int)min((long long)a.tokens_per_block, a.T - t0);
-  grid_dependency_wait();
-  grid_launch_dependents();
-  for (int j = threadIdx.x; j < nt * half; j += blockDim.x) {
-    const int i = j % half;
-    // angle in half turns, reduced to [-1, 1]
-    double turn = rope_position(a, (t0 + j / half) % a.pos_rows, i) * a.freq[i] * 0.31830988618379067154;
-    turn -= 2.0 * rint(0.5 * turn);
-    float s, c;
-    sincospif((float)turn, &s, &c);
-    cs[j] = make_float2(c, a.inverse ? -s : s);
-  }
-  __syncthreads();
+  const int t0 = blockIdx.x * a.tokens_per_block;
+  const int nt = min(a.tokens_per_block, a.T - t0);
   // places of a head that turn, then 16-byte (or single) pieces that do not
   const int turned = half / NP;
   constexpr int kCopy = VEC ? kVecN<T> : 1;
   const int items = turned + (a.D - a.R) / kCopy;
   const int per_pass = max(1, (int)blockDim.x / items);       // heads a pass of the block covers
   const int first = (int)threadIdx.x / items;
-  if (first >= per_pass) return;
-  const int passes = first < nh ? (nh - first + per_pass - 1) / per_pass : 0;
-  const long long x_step = per_pass * a.xh, y_step = per_pass * a.yh;
-  const T* x0 = static_cast<const T*>(a.x) + t0 * a.xt + (h0 + first) * a.xh;
-  T* y0 = static_cast<T*>(a.y) + t0 * a.yt + (h0 + first) * a.yh;
-  for (int item = (int)threadIdx.x - first * items; item < items; item += blockDim.x) {
-    if (item >= turned) {
-      const int at = a.R + (item - turned) * kCopy;
-      for (int k = 0; k < nt; ++k) {
-        const T* x = x0 + k * a.xt + at;
-        T* y = y0 + k * a.yt + at;
-        for (int j = 0; j < passes; ++j, x += x_step, y += y_step) {
-          if constexpr (VEC) *reinterpret_cast<uint4*>(y) = load_once(x);
-          else *y = *x;
+  int item = (int)threadIdx.x - first * items;
+  const bool works = first < per_pass;
+  const int at = HALVES ? item * NP : 2 * item * NP;
+  RopeCursor<const T> in = {static_cast<const T*>(a.x) + t0 * a.xt + (h0 + first) * a.xh, 0, first, per_pass * a.xh,
+                            a.xt - nh * a.xh};
+  RopeCursor<T> out = {static_cast<T*>(a.y) + t0 * a.yt + (h0 + first) * a.yh, 0, first, per_pass * a.yh,
+                       a.yt - nh * a.yh};
+  while (in.h >= nh) {           // more heads a pass than the block's tokens have
+    in.h -= nh;
+    ++in.k;
+    in.p += in.wrap;
+    out.h -= nh;
+    ++out.k;
+    out.p += out.wrap;
+  }
+  const RopeCursor<const T> in0 = in;
+  const RopeCursor<T> out0 = out;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  // the first rows are on their way while the angles are formed
+  typename Place::Raw r[kRows];
+  auto fetch = [&](typename Place::Raw (&r)[kRows]) {
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+      if (in.k < nt) {
+        Place::load(r[u], in.p + at, half);
+        in.next(per_pass, nh);
+      }
+  };
+  const bool turns = works && item < turned;
+  if (turns) fetch(r);
+  for (int j = threadIdx.x; j < nt * half; j += blockDim.x) {
+    const unsigned k = (unsigned)j / (unsigned)half, i = (unsigned)j - k * (unsigned)half;
+    unsigned p = (unsigned)t0 + k;
+    if (a.pos_rows != a.T) p %= (unsigned)a.pos_rows;
+    // angle in half turns, reduced to [-1, 1]
+    double turn = rope_position(a, p, (int)i) * a.freq[i] * 0.31830988618379067154;
+    turn -= 2.0 * rint(0.5 * turn);
+    float s, c;
+    sincospif((float)turn, &s, &c);
+    table[0][j] = c;
+    table[1][j] = a.inverse ? -s : s;
+  }
+  __syncthreads();
+  while (turns && out.k < nt) {
+    typename Place::Raw ahead[kRows];
+    fetch(ahead);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+      if (out.k < nt) {
+        typename Place::Turn w;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          w.c[i] = table[0][out.k * half + item * NP + i];
+          w.s[i] = table[1][out.k * half + item * NP + i];
         }
+        Place::turn(r[u], w, out.p + at, half);
+        out.next(per_pass, nh);
+        r[u] = ahead[u];
       }
-      continue;
-    }
-    const int at = HALVES ? item * NP : 2 * item * NP;
-    for (int k = 0; k < nt; ++k) {
-      const T* x = x0 + k * a.xt + at;
-      T* y = y0 + k * a.yt + at;
-      typename Place::Turn w;
+  }
+  if (!works) return;
+  // what passes unchanged, and (single pairs of a head wider than the block) the places past the block's threads
+  for (; item < items; item += blockDim.x) {
+    in = in0;
+    out = out0;
+    for (; out.k < nt; in.next(per_pass, nh), out.next(per_pass, nh)) {
+      if (item >= turned) {
+        const int c = a.R + (item - turned) * kCopy;
+        if constexpr (VEC) *reinterpret_cast<uint4*>(out.p + c) = load_once(in.p + c);
+        else out.p[c] = in.p[c];
+      } else if (item >= (int)blockDim.x) {
+        const int c = HALVES ? item * NP : 2 * item * NP;
+        typename Place::Raw raw;
+        typename Place::Turn w;
+        Place::load(raw, in.p + c, half);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float2 t = cs[k * half + item * NP + i];
-        w.c[i] = t.x;
-        w.s[i] = t.y;
-      }
-      for (int j = passes; j > 0; j -= kHeads) {
-        typename Place::Raw r[kHeads];
-#pragma unroll
-        for (int u = 0; u < kHeads; ++u)
-          if (u < j) {
-            Place::load(r[u], x, half);
-            x += x_step;
-          }
-#pragma unroll
-        for (int u = 0; u < kHeads; ++u)
-          if (u < j) {
-            Place::turn(r[u], w, y, half);
-            y += y_step;
-          }
+        for (int i = 0; i < NP; ++i) {
+          w.c[i] = table[0][out.k * half + item * NP + i];
+          w.s[i] = table[1][out.k * half + item * NP + i];
+        }
+        Place::turn(raw, w, out.p + c, half);
+      } else {
+        break;
       }
     }
   }
