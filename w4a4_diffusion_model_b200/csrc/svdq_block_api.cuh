@@ -57,12 +57,15 @@ svdq_status with_type(int dtype, F&& f) {
 
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
-// Kernels that stream rows through a ring (svdq_rows.cuh): stages for about
-// 48 KB of rows a block, at least one and at most kRingMaxStages of them.
-constexpr int kRingMaxBytes = 3 * 65536;   // one stage of two rows of 16384 fp32, and the backward pass's weight
+// Kernels that stream rows through a ring (svdq_rows.cuh) run 512 threads per SM
+// (640 in the backward pass up to 320 a block); the blocks share 192 KB, less
+// `other` bytes each, for their stages: at least one and at most kRingMaxStages.
+constexpr int kRingBytes = 3 * 65536;   // one stage of two rows of 16384 fp32, and the backward pass's weight
 
-int ring_depth(size_t stage_bytes) {
-  return (int)std::max<size_t>(1, std::min<size_t>(svdq::kRingMaxStages, 49152 / stage_bytes));
+int ring_depth(int threads, size_t stage_bytes, size_t other = 0) {
+  const int blocks = std::max(1, (other && threads <= 320 ? 640 : 512) / threads);
+  const size_t share = kRingBytes / blocks;
+  return (int)std::max<size_t>(1, std::min<size_t>(svdq::kRingMaxStages, (share - std::min(share, other)) / stage_bytes));
 }
 
 // Resident blocks per SM of a ring kernel; sets its shared-memory attribute.
@@ -70,7 +73,7 @@ template <auto KERN>
 int ring_blocks_per_sm(int threads, size_t smem) {
   static std::atomic<int> done[kMaxDevices];
   per_device_once(done, current_device(), [] {
-    if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMaxBytes) == cudaSuccess) return 1;
+    if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes) == cudaSuccess) return 1;
     cudaGetLastError();
     return 0;
   });
@@ -84,8 +87,9 @@ int ring_blocks_per_sm(int threads, size_t smem) {
 
 // Launches a ring kernel that takes rows in turn, `elems` elements a thread.
 template <auto KERN, typename Args>
-svdq_status launch_rows(const Args& a, int64_t rows, int64_t cols, int elems, size_t row_bytes, cudaStream_t st) {
+svdq_status launch_rows(Args a, int64_t rows, int64_t cols, int elems, size_t row_bytes, cudaStream_t st) {
   const int threads = round_up((int)((cols + elems - 1) / elems), 32);
+  a.depth = ring_depth(threads, row_bytes);
   const size_t smem = a.depth * row_bytes;
   const int64_t blocks = (int64_t)sm_count() * ring_blocks_per_sm<KERN>(threads, smem);
   cudaLaunchAttribute attr[1];
@@ -125,7 +129,7 @@ svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_
     return fail(SVDQ_ERR_MISALIGNED, "row stride %lld is not a multiple of 16 bytes", (long long)ldx);
   if ((r = check_device()) != SVDQ_OK) return r;
   if (M == 0) return SVDQ_OK;
-  svdq::Int8QuantArgs a{X, ldx, mult, static_cast<int8_t*>(Q), S, M, (int)K, 0};
+  const svdq::Int8QuantArgs a{X, ldx, mult, static_cast<int8_t*>(Q), S, M, (int)K, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return with_type(dtype, [&](auto tag) -> svdq_status {
     using T = typename decltype(tag)::type;
@@ -140,7 +144,6 @@ svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_
     }
     if (K <= 16384 && M > 2 * sms) {
       using namespace svdq;
-      a.depth = ring_depth((size_t)K * sizeof(T));
       const size_t row = (size_t)K * sizeof(T);
       if (K <= 2048) return launch_rows<int8_quantize_rows_kernel<T, 16, 4>>(a, M, K, 16, row, st);
       if (K <= 4096) return launch_rows<int8_quantize_rows_kernel<T, 32, 4>>(a, M, K, 32, row, st);
@@ -156,35 +159,9 @@ svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_
 }
 
 // ---------------------------------------------------------------- W8A8 product
-template <int NB, typename OT>
-svdq_status launch_int8_gemm(const svdq::Int8GemmArgs& args, const void* Qx, const void* Qw, int splits,
-                             cudaStream_t st) {
-  using C = svdq::Int8Cfg<NB>;
-  auto kern = svdq::svdq_int8_gemm_kernel<NB, OT>;
-  static std::atomic<int> done[kMaxDevices];
-  cudaError_t err = cudaSuccess;
-  per_device_once(done, current_device(), [&err, kern] {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes(C::kMany));
-    return err == cudaSuccess ? 1 : 0;
-  });
-  if (err != cudaSuccess)
-    return fail(SVDQ_ERR_CUDA, "cudaFuncSetAttribute(svdq_int8_gemm_kernel): %s", cudaGetErrorString(err));
-  svdq::Int8GemmArgs a = args;
-  a.a_rows = a.M >= 128 ? 128 : round_up(a.M, 8);
-  CUtensorMap tx, tw;
-  svdq_status r;
-  if ((r = make_tmap(&tx, Qx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.M, svdq::kI8KTile,
-                     (uint32_t)a.a_rows, CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
-    return r;
-  if ((r = make_tmap(&tw, Qw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N, svdq::kI8KTile, NB,
-                     CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
-    return r;
-  const int64_t tiles = (int64_t)((a.N + NB - 1) / NB) * ((a.M + 127) / 128);
-  if (tiles > (1ll << 31) - 1) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "too many tiles");
-  cudaLaunchAttribute attr[2];
-  a.stages = tiles * splits <= sm_count() ? C::kMany : C::kFew;
+cudaLaunchConfig_t int8_single_config(int64_t tiles, int splits, cudaStream_t st, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg =
-      pdl_config(dim3((unsigned)tiles, 1, (unsigned)splits), svdq::kI8Threads, C::bytes(a.stages), st, attr);
+      pdl_config(dim3((unsigned)tiles, 1, (unsigned)splits), svdq::kI8Threads, svdq::kI8Bytes, st, attr);
   if (splits > 1) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 1;
@@ -192,13 +169,57 @@ svdq_status launch_int8_gemm(const svdq::Int8GemmArgs& args, const void* Qx, con
     attr[1].val.clusterDim.z = splits;
     cfg.numAttrs = 2;
   }
-  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, tx, tw, a));
+  return cfg;
+}
+
+// Tiles of the single-CTA kernel that run at once with K split `splits` ways (0:
+// the kernel cannot run); also sets its shared-memory attribute.
+template <typename OT>
+int int8_single_tiles(int splits) {
+  static std::atomic<int> cache[3][kMaxDevices];
+  return per_device_once(cache[splits / 2], current_device(), [splits] {   // splits 1, 2, 4
+    auto kern = svdq::svdq_int8_gemm_kernel<OT>;
+    int n = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, svdq::kI8Bytes) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = int8_single_config(1, splits, nullptr, attr);
+    if (splits == 1) return sm_count() + 1;
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, (void*)kern, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    return n + 1;
+  }) - 1;
+}
+
+template <typename OT>
+svdq_status launch_int8_single(const svdq::Int8GemmArgs& args, const void* Qx, const void* Qw, int splits,
+                               cudaStream_t st) {
+  svdq::Int8GemmArgs a = args;
+  a.a_rows = a.M >= 128 ? 128 : round_up(a.M, 8);
+  CUtensorMap tx, tw;
+  svdq_status r;
+  if ((r = make_tmap(&tx, Qx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.M, svdq::kI8KTile,
+                     (uint32_t)a.a_rows, CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
+    return r;
+  if ((r = make_tmap(&tw, Qw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N, svdq::kI8KTile,
+                     svdq::kI8Cols, CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
+    return r;
+  const int64_t tiles = (int64_t)((a.N + svdq::kI8Cols - 1) / svdq::kI8Cols) * ((a.M + 127) / 128);
+  if (tiles > (1ll << 31) - 1) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "too many tiles");
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = int8_single_config(tiles, splits, st, attr);
+  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::svdq_int8_gemm_kernel<OT>, tx, tw, a));
   return SVDQ_OK;
 }
 
-template <int NB>
 cudaLaunchConfig_t int8_pair_config(int clusters, cudaStream_t st, cudaLaunchAttribute* attr) {
-  cudaLaunchConfig_t cfg = pdl_config(2 * clusters, svdq::kP8Threads, svdq::Int8PairCfg<NB>::kBytes, st, attr);
+  cudaLaunchConfig_t cfg = pdl_config(2 * clusters, svdq::kP8Threads, svdq::kP8Bytes, st, attr);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = 2;
   attr[1].val.clusterDim.y = 1;
@@ -209,17 +230,17 @@ cudaLaunchConfig_t int8_pair_config(int clusters, cudaStream_t st, cudaLaunchAtt
 
 // Clusters of the pair kernel that fit on the device at once (0: none); also
 // sets the kernel's shared-memory attribute there.
-template <int NB, typename OT>
+template <typename OT>
 int int8_pair_clusters() {
   static std::atomic<int> cache[kMaxDevices];
   return per_device_once(cache, current_device(), [] {
-    auto kern = svdq::svdq_int8_gemm_pair_kernel<NB, OT>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, svdq::Int8PairCfg<NB>::kBytes) != cudaSuccess) {
+    auto kern = svdq::svdq_int8_gemm_pair_kernel<OT>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, svdq::kP8Bytes) != cudaSuccess) {
       cudaGetLastError();
       return 0;
     }
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = int8_pair_config<NB>(sm_count() / 2, nullptr, attr);
+    cudaLaunchConfig_t cfg = int8_pair_config(sm_count() / 2, nullptr, attr);
     std::swap(attr[0], attr[1]);
     cfg.numAttrs = 1;
     int n = 0;
@@ -231,7 +252,7 @@ int int8_pair_clusters() {
   }) - 1;
 }
 
-template <int NB, typename OT>
+template <typename OT>
 svdq_status launch_int8_pair(const svdq::Int8GemmArgs& a, const void* Qx, const void* Qw, int clusters,
                              cudaStream_t st) {
   CUtensorMap tx, tw, ty;
@@ -239,7 +260,7 @@ svdq_status launch_int8_pair(const svdq::Int8GemmArgs& a, const void* Qx, const 
   if ((r = make_tmap(&tx, Qx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.M, svdq::kI8KTile, 128,
                      CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
     return r;
-  if ((r = make_tmap(&tw, Qw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N, svdq::kI8KTile, NB / 2,
+  if ((r = make_tmap(&tw, Qw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.K, (uint64_t)a.N, svdq::kI8KTile, 128,
                      CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
     return r;
   const uint64_t ld = a.M > 1 ? (uint64_t)a.ldy : (uint64_t)a.N;
@@ -248,10 +269,10 @@ svdq_status launch_int8_pair(const svdq::Int8GemmArgs& a, const void* Qx, const 
   if (tma_y && (r = make_tmap(&ty, a.y, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.N * sizeof(OT), (uint64_t)a.M,
                               128, 32, CU_TENSOR_MAP_SWIZZLE_128B, ld * sizeof(OT))) != SVDQ_OK)
     return r;
-  const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + NB - 1) / NB);
+  const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = int8_pair_config<NB>((int)std::min<int64_t>(tiles, clusters), st, attr);
-  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::svdq_int8_gemm_pair_kernel<NB, OT>, tx, tw, ty, a, tma_y ? 1 : 0));
+  cudaLaunchConfig_t cfg = int8_pair_config((int)std::min<int64_t>(tiles, clusters), st, attr);
+  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::svdq_int8_gemm_pair_kernel<OT>, tx, tw, ty, a, tma_y ? 1 : 0));
   return SVDQ_OK;
 }
 
@@ -268,22 +289,52 @@ svdq_status launch_int8_few(const svdq::Int8GemmArgs& a, const void* Qx, const v
   return SVDQ_OK;
 }
 
-// Which kernel and split serves a product (environment override for sweeps).
+// Which kernel serves a product, by estimated microseconds on this GPU. The
+// constants are fits to sweeps over M 1..4608, K 1024..13824, N 1024..24576:
+//   0.29 us per 128 bytes of K and wave, whatever the tile (see the kernels);
+//   6.2e6 weight bytes per us where HBM bounds it;
+//   a fixed part of 5.7 for CTA pairs, and for single CTAs 5.1 + 0.033 per row
+//   of the tile with K whole, 5.0 + 0.055 with K halved, 5.7 + 0.046 with K in
+//   quarters (the cluster's sum). Measured, us, pairs against the best single:
+//   16 x 4096 x 4096 15 / 8.8, 64 x 4096 x 24576 29 / 23, 128 x 4096 x 4096
+//   15.4 / 13.8, 128 x 4096 x 12288 17 / 20, 333 x 1360 x 2304 9.7 / 11.5,
+//   1024 x 4096 x 4096 16 / 22.
+// Single CTAs are considered for one wave only: with every SM busy their tiles
+// fetch half as much again per product as a pair's.
 template <typename OT>
 svdq_status launch_int8_linear(const svdq::Int8GemmArgs& a, const void* Qx, const void* Qw, cudaStream_t st) {
-  const char* f = getenv("SVDQ_I8");
-  int mode = f ? atoi(f) : 0;      // 1: pair, 2: few, 1xxs: NB=64 splits s, 2xxs: NB=128
-  if (mode == 0) mode = a.M <= 8 ? 2 : (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256) >= 37 ? 1 : 201;
-  if (mode == 1) return launch_int8_pair<256, OT>(a, Qx, Qw, int8_pair_clusters<256, OT>(), st);
-  if (mode == 3) return launch_int8_pair<128, OT>(a, Qx, Qw, int8_pair_clusters<128, OT>(), st);
-  if (mode == 2) {
+  const int64_t weights = (int64_t)a.N * a.K;
+  // Up to 8 tokens: the dot-product kernel costs 2 us + 0.13 (one token), 0.16
+  // (two), 0.21 (four) or 0.37 us (eight) per 2^20 weights; the single-CTA kernel
+  // 21 us at 4096 x 24576 and 8.8 at 4096 x 4096, which eight and four tokens
+  // reach at the sizes below (measured 8.0 us for 8 x 4096 x 4096).
+  if (a.M <= 2 || (a.M <= 4 && weights <= (1ll << 26)) || (a.M <= 8 && weights <= (1ll << 24))) {
     if (a.M == 1) return launch_int8_few<1, OT>(a, Qx, Qw, st);
     if (a.M == 2) return launch_int8_few<2, OT>(a, Qx, Qw, st);
     if (a.M <= 4) return launch_int8_few<4, OT>(a, Qx, Qw, st);
     return launch_int8_few<8, OT>(a, Qx, Qw, st);
   }
-  if (mode / 100 == 1) return launch_int8_gemm<64, OT>(a, Qx, Qw, mode % 100, st);
-  return launch_int8_gemm<128, OT>(a, Qx, Qw, mode % 100, st);
+  const double k_us = 0.29 * ((a.K + svdq::kI8KTile - 1) / svdq::kI8KTile), hbm_us = (double)weights / 6.2e6;
+  const int clusters = int8_pair_clusters<OT>();
+  const int64_t pairs = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+  const int64_t tiles = (int64_t)((a.M + 127) / 128) * ((a.N + svdq::kI8Cols - 1) / svdq::kI8Cols);
+  if (pairs > (1ll << 30)) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "too many tiles");
+  int best = clusters > 0 ? 0 : 1;               // 0: pairs, else single CTAs with K split that many ways
+  double best_us = clusters > 0 ? 5.7 + std::max(hbm_us, k_us * (double)((pairs + clusters - 1) / clusters)) : 1e30;
+  const double rows = (double)std::min(a.M, 128), fixed[3] = {5.1 + 0.033 * rows, 5.0 + 0.055 * rows, 5.7 + 0.046 * rows};
+  for (int i = 0; i < 3; ++i) {
+    const int splits = 1 << i;
+    if (a.K < 2 * splits * svdq::kI8KTile && splits > 1) break;
+    if (tiles > int8_single_tiles<OT>(splits)) break;
+    const double us = fixed[i] + std::max(hbm_us, k_us / splits);
+    if (us < best_us) {
+      best_us = us;
+      best = splits;
+    }
+  }
+  if (best == 0) return launch_int8_pair<OT>(a, Qx, Qw, clusters, st);
+  if (int8_single_tiles<OT>(best) <= 0) return fail(SVDQ_ERR_CUDA, "svdq_int8_gemm_kernel cannot run on this device");
+  return launch_int8_single<OT>(a, Qx, Qw, best, st);
 }
 
 // ---------------------------------------------------------------- norm
@@ -358,13 +409,11 @@ svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStr
     if constexpr (VEC) {
       if (n.C > 512 && n.M > 2 * sm_count()) {
         using namespace svdq;
-        NormArgs r = a;
         const size_t row = (size_t)n.C * sizeof(T);
-        r.depth = ring_depth(row);
-        if (n.C <= 2048) return launch_rows<layernorm_rows_kernel<T, WT, 16, 4, QUANT>>(r, n.M, n.C, 16, row, st);
-        if (n.C <= 4096) return launch_rows<layernorm_rows_kernel<T, WT, 32, 4, QUANT>>(r, n.M, n.C, 32, row, st);
-        if (n.C <= 8192) return launch_rows<layernorm_rows_kernel<T, WT, 32, 8, QUANT>>(r, n.M, n.C, 32, row, st);
-        return launch_rows<layernorm_rows_kernel<T, WT, 32, 16, QUANT>>(r, n.M, n.C, 32, row, st);
+        if (n.C <= 2048) return launch_rows<layernorm_rows_kernel<T, WT, 16, 4, QUANT>>(a, n.M, n.C, 16, row, st);
+        if (n.C <= 4096) return launch_rows<layernorm_rows_kernel<T, WT, 32, 4, QUANT>>(a, n.M, n.C, 32, row, st);
+        if (n.C <= 8192) return launch_rows<layernorm_rows_kernel<T, WT, 32, 8, QUANT>>(a, n.M, n.C, 32, row, st);
+        return launch_rows<layernorm_rows_kernel<T, WT, 32, 16, QUANT>>(a, n.M, n.C, 32, row, st);
       }
     }
     return norm_width<VEC>(pieces, [&](auto nv, auto maxt) -> svdq_status {
@@ -459,7 +508,7 @@ svdq_status svdq_int8_linear(int64_t M, int64_t K, int64_t N, const void* Qx, co
   if ((r = check_rows("Y", M, N, ldy)) != SVDQ_OK) return r;
   if ((r = check_device()) != SVDQ_OK) return r;
   if (M == 0) return SVDQ_OK;
-  const svdq::Int8GemmArgs a{Sx, Sw, bias, Y, ldy, (int)M, (int)N, (int)K, 0, 0};
+  const svdq::Int8GemmArgs a{Sx, Sw, bias, Y, ldy, (int)M, (int)N, (int)K, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return with_type(y_dtype, [&](auto tag) -> svdq_status {
     using T = typename decltype(tag)::type;
@@ -563,10 +612,10 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
       if (n.C > 512) {
         using namespace svdq;
         const size_t rows = 2 * (size_t)n.C * sizeof(T);
-        a.depth = ring_depth(rows);
         auto go = [&](auto kern_c, int elems) -> svdq_status {
           constexpr auto kern = decltype(kern_c)::value;
           const int threads = round_up(((int)n.C + elems - 1) / elems, 32);
+          a.depth = ring_depth(threads, rows, (size_t)n.C * 4);
           const size_t smem = a.depth * rows + (size_t)n.C * 4;
           ring_blocks_per_sm<kern>(threads, smem);   // sets the attribute
           cudaLaunchAttribute attr[1];

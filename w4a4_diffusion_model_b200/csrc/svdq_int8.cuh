@@ -203,7 +203,6 @@ struct Int8GemmArgs {
   long long ldy;
   int M, N, K;
   int a_rows;          // single-CTA kernel: rows of the A box (8..128)
-  int stages;          // single-CTA kernel: stages of its ring
 };
 
 // ---------------------------------------------------------------- few tokens
@@ -232,16 +231,13 @@ __global__ void __launch_bounds__(kGvThreads) int8_few_tokens_kernel(const int8_
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[c][m] = 0;
   const int8_t* w = qw + (long long)n0 * a.K;
-  bool waited = false;
+  grid_dependency_wait();
+  grid_launch_dependents();
   for (int k = wk * 512 + lane * 16; k < a.K; k += warps_k * 512) {
     uint4 r[kGvChannels];
 #pragma unroll
     for (int c = 0; c < kGvChannels; ++c)
       r[c] = n0 + c < a.N ? load_once(w + (long long)c * a.K + k) : make_uint4(0, 0, 0, 0);
-    if (!waited) {   // the weights are no earlier kernel's output: their first loads go ahead of the wait
-      grid_dependency_wait();
-      waited = true;
-    }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const uint4 x = m < a.M ? *reinterpret_cast<const uint4*>(qx + (long long)m * a.K + k) : make_uint4(0, 0, 0, 0);
@@ -255,8 +251,6 @@ __global__ void __launch_bounds__(kGvThreads) int8_few_tokens_kernel(const int8_
       }
     }
   }
-  if (!waited) grid_dependency_wait();
-  grid_launch_dependents();
   __syncwarp();
 #pragma unroll
   for (int c = 0; c < kGvChannels; ++c)
@@ -278,65 +272,69 @@ __global__ void __launch_bounds__(kGvThreads) int8_few_tokens_kernel(const int8_
 }
 
 // ---------------------------------------------------------------- single-CTA kernel
-// One 128 x NB output tile per CTA and K slice; a cluster of gridDim.z CTAs
-// splits K when there are too few tiles for the GPU. Warp 0 loads (TMA, 128
-// bytes of K per stage), warp 1 issues the MMAs, then all eight warps take the
-// accumulator out of tensor memory (warp w: lanes 32 (w % 4).., half of the
-// columns) into shared memory (the ring's, idle by then). The CTAs of a cluster
-// read each other's tiles there: CTA z adds and writes the columns
-// [z, z + 1) NB / gridDim.z. A lane keeps its columns and their scales from row
-// to row. Rows past M are neither loaded (the A box is cut to a_rows) nor
-// written, so few tokens cost little traffic.
+// One 128 x 256 output tile per CTA and K slice; a cluster of gridDim.z CTAs
+// splits K when there are too few tiles for the GPU. The tile is that wide
+// because an 8-bit integer MMA of 32 K elements takes about 128 cycles whatever
+// its N (measured: 0.28 us per 128 bytes of K for 128 x 64, 128 x 128 and
+// 256 x 256 tiles alike, one accumulator or four), so narrow tiles only repeat
+// it; what shortens a small product is a shorter K slice.
+//
+// Warp 0 loads (TMA, 128 bytes of K per stage), warp 1 issues the MMAs, then all
+// eight warps take the accumulator out of tensor memory (warp w: lanes
+// 32 (w % 4).., half of the columns) into shared memory (the ring's, idle by
+// then). The CTAs of a cluster read each other's tiles there: CTA z adds and
+// writes the columns [z, z + 1) 256 / gridDim.z. A lane keeps its columns and
+// their scales from row to row. Rows past M are neither loaded (the A box is cut
+// to a_rows) nor written, so few tokens cost little traffic.
 constexpr int kI8KTile = 128;                        // K elements (= bytes) per stage row
 constexpr int kI8StageA = 128 * kI8KTile;            // 16 KB
 constexpr int kI8Threads = 256;
+constexpr int kI8Cols = 256;
+constexpr int kI8StageBytes = kI8StageA + kI8Cols * kI8KTile;   // 48 KB
+constexpr int kI8Stages = 4;
+constexpr int kI8Ld = kI8Cols + 4;                   // int32 per row of the staged tile
+static_assert(kI8Stages * kI8StageBytes >= 128 * kI8Ld * 4, "the tile is staged in the ring");
+constexpr int kI8ScaleOffset = kI8Stages * kI8StageBytes;   // sx of the rows, then (sw, bias) of the columns
+constexpr int kI8BarOffset = kI8ScaleOffset + 128 * 4 + kI8Cols * 8;
+constexpr int kI8Bytes = kI8BarOffset + 128 + 1024;
 
-// The ring follows the barriers in shared memory; it has `few` stages where two
-// CTAs share an SM and `many` where each has one to itself (what is in flight
-// bounds a CTA's rate: 96 KB of it).
-template <int NB>
-struct Int8Cfg {
-  static constexpr int kStageB = NB * kI8KTile;
-  static constexpr int kStageBytes = kI8StageA + kStageB;
-  static constexpr int kFew = NB == 64 ? 4 : 3, kMany = NB == 64 ? 8 : 6;
-  static constexpr int kLd = NB + 4;                 // int32 per row of the staged tile
-  static constexpr int kTileBytes = 128 * kLd * 4;
-  static_assert(kFew * kStageBytes >= kTileBytes, "the tile is staged in the ring");
-  static constexpr int bytes(int stages) { return 1024 + 1024 + stages * kStageBytes; }
-};
-
-__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+// Sum over a cluster's CTAs of the int32 at the same shared address; `first` is
+// this CTA's.
+__device__ __forceinline__ int4 sum_cluster(int4 first, uint32_t addr, int z, int splits) {
+  for (int p = 1; p < splits; ++p) {
+    int4 u;
+    asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "r"(mapa_shared(addr, (uint32_t)((z + p) % splits)))
+                 : "memory");
+    first.x += u.x;
+    first.y += u.y;
+    first.z += u.z;
+    first.w += u.w;
+  }
+  return first;
 }
 
-template <int NB, typename OT>
-__global__ void __launch_bounds__(kI8Threads) svdq_int8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x,
-                                                                    const __grid_constant__ CUtensorMap tm_w,
-                                                                    const Int8GemmArgs a) {
-  using C = Int8Cfg<NB>;
+template <typename OT>
+__global__ void __launch_bounds__(kI8Threads, 1) svdq_int8_gemm_kernel(const __grid_constant__ CUtensorMap tm_x,
+                                                                       const __grid_constant__ CUtensorMap tm_w,
+                                                                       const Int8GemmArgs a) {
   extern __shared__ __align__(1024) unsigned char i8_smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(i8_smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
-  uint64_t* empty = full + C::kMany;
-  uint64_t* done = empty + C::kMany;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kI8BarOffset);
+  uint64_t* empty = full + kI8Stages;
+  uint64_t* done = empty + kI8Stages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  smem += 1024;
-  const int stages = a.stages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tiles_n = (a.N + NB - 1) / NB;
-  const int n0 = (int)(blockIdx.x % tiles_n) * NB, m0 = (int)(blockIdx.x / tiles_n) * 128;
+  const int tiles_n = (a.N + kI8Cols - 1) / kI8Cols;
+  const int n0 = (int)(blockIdx.x % tiles_n) * kI8Cols, m0 = (int)(blockIdx.x / tiles_n) * 128;
   const int splits = gridDim.z, z = blockIdx.z;
   const int kts = (a.K + kI8KTile - 1) / kI8KTile;
-  const int kt0 = (int)((long long)kts * z / splits), kt1 = (int)((long long)kts * (z + 1) / splits);
+  const int kt0 = kts * z / splits, kt1 = kts * (z + 1) / splits;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
+    for (int s = 0; s < kI8Stages; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
@@ -346,7 +344,7 @@ __global__ void __launch_bounds__(kI8Threads) svdq_int8_gemm_kernel(const __grid
     prefetch_tmap(&tm_w);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, NB);
+    tmem_alloc(tmem_slot, kI8Cols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -357,43 +355,56 @@ __global__ void __launch_bounds__(kI8Threads) svdq_int8_gemm_kernel(const __grid
   grid_launch_dependents();
 
   if (warp == 0 && lane == 0) {
-    const uint32_t bytes = (uint32_t)(a.a_rows * kI8KTile + C::kStageB);
+    const uint32_t bytes = (uint32_t)((a.a_rows + kI8Cols) * kI8KTile);
     int s = 0, kt = kt0;
     uint32_t ph = 1;
     for (; kt < kt1; ++kt) {
       if (!mbar_wait(empty + s, ph, kDevErrTimeoutEmpty)) break;
-      unsigned char* sa = smem + s * C::kStageBytes;
+      unsigned char* sa = smem + s * kI8StageBytes;
       mbar_arrive_expect_tx(full + s, bytes);
-      tma_load_2d(sa, &tm_x, full + s, kt * kI8KTile, m0);
       tma_load_2d(sa + kI8StageA, &tm_w, full + s, kt * kI8KTile, n0);
-      if (++s == stages) {
+      tma_load_2d(sa, &tm_x, full + s, kt * kI8KTile, m0);
+      if (++s == kI8Stages) {
         s = 0;
         ph ^= 1u;
       }
     }
     if (device_error_set()) {   // let the copies this thread issued land before the CTA exits
       const int it = kt - kt0;
-      for (int j = it > stages ? it - stages : 0; j < it; ++j) mbar_drain(full + j % stages, (j / stages) & 1);
+      for (int j = it > kI8Stages ? it - kI8Stages : 0; j < it; ++j) mbar_drain(full + j % kI8Stages, (j / kI8Stages) & 1);
     }
   } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = idesc_i8(128, NB);
+    const uint32_t idesc = idesc_i8(128, kI8Cols);
     int s = 0;
     uint32_t ph = 0;
     for (int kt = kt0; kt < kt1; ++kt) {
       if (!mbar_wait(full + s, ph, kDevErrTimeoutFull)) break;
       tc_fence_after();
-      const uint64_t ad = smem_desc(smem_u32(smem + s * C::kStageBytes), 16, 1024, kSwizzle128B);
-      const uint64_t bd = smem_desc(smem_u32(smem + s * C::kStageBytes + kI8StageA), 16, 1024, kSwizzle128B);
+      const uint64_t ad = smem_desc(smem_u32(smem + s * kI8StageBytes), 16, 1024, kSwizzle128B);
+      const uint64_t bd = smem_desc(smem_u32(smem + s * kI8StageBytes + kI8StageA), 16, 1024, kSwizzle128B);
+      const int steps = min(kI8KTile, a.K - kt * kI8KTile + 31) / 32;   // of 32 K elements (32 bytes)
 #pragma unroll
-      for (int j = 0; j < kI8KTile / 32; ++j)   // 32 K elements (32 bytes) per MMA
-        mma_i8(tmem, ad + 2u * j, bd + 2u * j, idesc, kt > kt0 || j > 0 ? 1u : 0u);
+      for (int j = 0; j < kI8KTile / 32; ++j)
+        if (j < steps) mma_i8(tmem, ad + 2u * j, bd + 2u * j, idesc, kt > kt0 || j > 0 ? 1u : 0u);
       tc_commit(empty + s);
-      if (++s == stages) {
+      if (++s == kI8Stages) {
         s = 0;
         ph ^= 1u;
       }
     }
     tc_commit(done);
+  }
+  float* sxs = reinterpret_cast<float*>(smem + kI8ScaleOffset);
+  float2* cols_s = reinterpret_cast<float2*>(smem + kI8ScaleOffset + 128 * 4);
+  if (warp >= 2) {   // the scales, while the product runs
+    for (int i = threadIdx.x - 64; i < 128 + kI8Cols; i += kI8Threads - 64) {
+      if (i < 128) {
+        sxs[i] = m0 + i < a.M ? a.sx[m0 + i] : 0.f;
+      } else {
+        const int n = n0 + i - 128;
+        cols_s[i - 128] = n < a.N ? make_float2(a.sw[n], a.bias ? a.bias[n] : 0.f) : make_float2(0.f, 0.f);
+      }
+    }
   }
   __syncwarp();
   // every MMA has read its stages: the ring is free for the tile
@@ -401,77 +412,76 @@ __global__ void __launch_bounds__(kI8Threads) svdq_int8_gemm_kernel(const __grid
   tc_fence_after();
   const int q = warp & 3;
   if (ok && 32 * q < a.M - m0) {
-    int* tile = reinterpret_cast<int*>(smem) + (32 * q + lane) * C::kLd;
+    int* tile = reinterpret_cast<int*>(smem) + (32 * q + lane) * kI8Ld;
 #pragma unroll
-    for (int c = (warp >> 2) * (NB / 2); c < ((warp >> 2) + 1) * (NB / 2); c += 32) {
+    for (int i = 0; i < kI8Cols / 2; i += 32) {
+      const int c = (warp >> 2) * (kI8Cols / 2) + i;
       uint32_t v[32];
       tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + c, v);
       tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 32; i += 4)
-        *reinterpret_cast<uint4*>(tile + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<uint4*>(tile + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     }
   }
   tc_fence_before();
   if (splits > 1) cluster_sync();
   else __syncthreads();
   if (ok) {
-    // a lane's four columns: neighbours where Y's rows allow wide stores, else
-    // a quarter of the columns apart, so that a warp's single stores are dense
-    const int rows = min(128, a.M - m0), cols = NB / splits, per_row = cols / 4;
+    // A warp takes up to 128 of the CTA's columns, four a lane: neighbours where
+    // Y's rows allow wide stores, else a quarter of the columns apart, so that a
+    // warp's single stores are dense (the cluster's sums, read four at a time,
+    // then pass through this CTA's own columns of its tile, which no peer reads).
+    const int rows = min(128, a.M - m0), cols = min(128, kI8Cols / splits), per_row = cols / 4;
     const bool wide = (a.ldy & 3) == 0;
-    const int place = lane % per_row;
-    const int c0 = z * cols + (wide ? 4 * place : place), dc = wide ? 1 : per_row;
-    float sw[4], bias[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = min(n0 + c0 + i * dc, a.N - 1);
-      sw[i] = a.sw[n];
-      bias[i] = a.bias ? a.bias[n] : 0.f;
-    }
-    const int rows_per_warp = 32 / per_row;
+    const int place = lane % per_row, dc = wide ? 1 : per_row;
+    const int rows_per_warp = 32 / per_row, row_step = (kI8Threads / 32) * rows_per_warp;
+    const int row0 = warp * rows_per_warp + lane / per_row;
     const uint32_t base = smem_u32(smem);
-    OT* y = static_cast<OT*>(a.y) + (long long)m0 * a.ldy + n0 + c0;
-#pragma unroll 2
-    for (int r = warp * rows_per_warp + lane / per_row; r < rows; r += (kI8Threads / 32) * rows_per_warp) {
-      const uint32_t at = (uint32_t)(r * C::kLd + c0) * 4;
-      int t[4];
-      if (wide) {
-        int4 v = *reinterpret_cast<const int4*>(smem + at);
-        for (int p = 1; p < splits; ++p) {
-          const int4 u = ld_cluster_int4(mapa_shared(base + at, (uint32_t)((z + p) % splits)));
-          v.x += u.x;
-          v.y += u.y;
-          v.z += u.z;
-          v.w += u.w;
+    for (int part = 0; part < kI8Cols / splits; part += cols) {
+      const int first = z * (kI8Cols / splits) + part;
+      if (!wide && splits > 1) {
+#pragma unroll 4
+        for (int r = row0; r < rows; r += row_step) {
+          const uint32_t at = (uint32_t)(r * kI8Ld + first + 4 * place) * 4;
+          *reinterpret_cast<int4*>(smem + at) =
+              sum_cluster(*reinterpret_cast<const int4*>(smem + at), base + at, z, splits);
         }
-        t[0] = v.x; t[1] = v.y; t[2] = v.z; t[3] = v.w;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          t[i] = *reinterpret_cast<const int*>(smem + at + 4 * i * dc);
-          for (int p = 1; p < splits; ++p) {
-            int u;
-            asm volatile("ld.shared::cluster.b32 %0, [%1];"
-                         : "=r"(u)
-                         : "r"(mapa_shared(base + at + 4 * i * dc, (uint32_t)((z + p) % splits)))
-                         : "memory");
-            t[i] += u;
-          }
-        }
+        __syncwarp();
       }
-      const float sx = a.sx[m0 + r];
-      float f[4];
+      const int c0 = first + (wide ? 4 * place : place);
+      float sw[4], bias[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = fmaf((float)t[i] * sw[i], sx, bias[i]);
-      OT* p = y + (long long)r * a.ldy;
-      if (wide && n0 + c0 + 4 <= a.N) {
-        if constexpr (sizeof(OT) == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-        else *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0], f[1], OT()), pack2(f[2], f[3], OT()));
-      } else {
+      for (int i = 0; i < 4; ++i) {
+        const float2 sb = cols_s[c0 + i * dc];
+        sw[i] = sb.x;
+        bias[i] = sb.y;
+      }
+      OT* y = static_cast<OT*>(a.y) + (long long)m0 * a.ldy + n0 + c0;
+#pragma unroll 4
+      for (int r = row0; r < rows; r += row_step) {
+        const uint32_t at = (uint32_t)(r * kI8Ld + c0) * 4;
+        int t[4];
+        if (wide) {
+          const int4 v = sum_cluster(*reinterpret_cast<const int4*>(smem + at), base + at, z, splits);
+          t[0] = v.x; t[1] = v.y; t[2] = v.z; t[3] = v.w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n0 + c0 + i * dc < a.N) p[i * dc] = from_float<OT>(f[i]);
+          for (int i = 0; i < 4; ++i) t[i] = *reinterpret_cast<const int*>(smem + at + 4 * i * dc);
+        }
+        const float sx = sxs[r];
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = fmaf((float)t[i] * sw[i], sx, bias[i]);
+        OT* p = y + (long long)r * a.ldy;
+        if (wide && n0 + c0 + 4 <= a.N) {
+          if constexpr (sizeof(OT) == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+          else *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0], f[1], OT()), pack2(f[2], f[3], OT()));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n0 + c0 + i * dc < a.N) p[i * dc] = from_float<OT>(f[i]);
+        }
       }
     }
   }
@@ -479,20 +489,19 @@ __global__ void __launch_bounds__(kI8Threads) svdq_int8_gemm_kernel(const __grid
   else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, NB);
+    tmem_dealloc(tmem, kI8Cols);
   }
 }
 
 // ---------------------------------------------------------------- CTA-pair kernel
 // Large products: one tcgen05 MMA (cta_group::2) spans the two SMs of a cluster
-// of 2 and computes a 256 x NB tile (NB = 256, or 128 where that fills more SMs);
-// each CTA stages its own 128 rows of X and its own NB / 2 rows of W (at NB = 256
-// half of what two single CTAs would fetch for the same tile). Persistent:
-// cluster c takes tiles c, c + clusters, ...; two accumulators alternate, so a
-// tile's epilogue runs under the next tile's MMAs.
+// of 2 and computes a 256 x 256 tile; each CTA stages its own 128 rows of X and its
+// own 128 rows of W (two thirds of the bytes that a 128 x 256 tile would fetch
+// per product). Persistent: cluster c takes tiles c, c + clusters, ...; two
+// accumulators alternate, so a tile's epilogue runs under the next tile's MMAs.
 // Roles per CTA (320 threads):
 //   warps 0-7  epilogue: warp (q, h) takes accumulator lanes 32q.. and columns
-//              h NB/2..: scales, bias, rounding, 128B-swizzled boxes, TMA stores
+//              128 h..: scales, bias, rounding, 128B-swizzled boxes, TMA stores
 //   warp 8     producer: TMA loads of this CTA's rows, counted on the even
 //              CTA's stage barrier (both CTAs' bytes)
 //   warp 9     the even CTA's lane 0 issues the MMAs; a multicast commit frees
@@ -502,18 +511,14 @@ __global__ void __launch_bounds__(kI8Threads) svdq_int8_gemm_kernel(const __grid
 constexpr int kP8Threads = 320;
 constexpr int kP8EpiWarps = 8;
 constexpr int kP8Band = 8;
+constexpr int kP8StageBytes = 2 * 128 * kI8KTile;            // 32 KB: 128 rows of X, 128 rows of W
+constexpr int kP8Stages = 5;
 constexpr int kP8BoxBytes = 4096;                            // 32 rows x 128 bytes
-
-template <int NB>
-struct Int8PairCfg {
-  static constexpr int kStageBytes = (128 + NB / 2) * kI8KTile;   // 32 | 24 KB
-  static constexpr int kStages = NB == 256 ? 5 : 7;
-  static constexpr int kCols = NB / 2;                            // accumulator columns per epilogue warp
-  static constexpr int kBoxOffset = kStages * kStageBytes;
-  static constexpr int kColOffset = kBoxOffset + kP8EpiWarps * kP8BoxBytes;   // (sw, bias) of each warp's columns
-  static constexpr int kBarOffset = kColOffset + kP8EpiWarps * kCols * 8;
-  static constexpr int kBytes = kBarOffset + 256 + 1024;
-};
+constexpr int kP8Cols = 128;                                 // accumulator columns per epilogue warp
+constexpr int kP8BoxOffset = kP8Stages * kP8StageBytes;
+constexpr int kP8ColOffset = kP8BoxOffset + kP8EpiWarps * kP8BoxBytes;   // (sw, bias) of each warp's columns
+constexpr int kP8BarOffset = kP8ColOffset + kP8EpiWarps * kP8Cols * 8;
+constexpr int kP8Bytes = kP8BarOffset + 256 + 1024;
 
 __device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
@@ -538,27 +543,24 @@ struct Int8Tile {
   int m0, n0;
 };
 
-template <int NB>
 __device__ __forceinline__ Int8Tile int8_pair_tile(int tile, int tiles_m, int tiles_n) {
   const int band = tile / (kP8Band * tiles_n);
   const int rows = min(kP8Band, tiles_m - band * kP8Band);
   const int i = tile - band * kP8Band * tiles_n;
-  return Int8Tile{(band * kP8Band + i % rows) * 256, (i / rows) * NB};
+  return Int8Tile{(band * kP8Band + i % rows) * 256, (i / rows) * 256};
 }
 
 // tm_y views Y as bytes, in boxes of 32 rows x 128; tma_y = 0 where Y's address or
 // row stride does not allow it (then the staged boxes are written by plain stores).
-template <int NB, typename OT>
+template <typename OT>
 __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x,
                                                                             const __grid_constant__ CUtensorMap tm_w,
                                                                             const __grid_constant__ CUtensorMap tm_y,
                                                                             const Int8GemmArgs a, int tma_y) {
-  using C = Int8PairCfg<NB>;
-  constexpr int kP8Stages = C::kStages, kP8StageBytes = C::kStageBytes;
   extern __shared__ __align__(1024) unsigned char p8_smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(p8_smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);   // even CTA: both CTAs' loads
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kP8BarOffset);   // even CTA: both CTAs' loads
   uint64_t* empty = full + kP8Stages;
   uint64_t* acc_full = empty + kP8Stages;    // [2]
   uint64_t* acc_empty = acc_full + 2;        // [2], even CTA: both CTAs' epilogue warps
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
   const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
-  const int tiles_m = (a.M + 255) / 256, tiles_n = (a.N + NB - 1) / NB;
+  const int tiles_m = (a.M + 255) / 256, tiles_n = (a.N + 255) / 256;
   const int ntiles = tiles_m * tiles_n;
   const int kts = (a.K + kI8KTile - 1) / kI8KTile;
 
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
     if (tma_y) prefetch_tmap(&tm_y);
   }
   if (warp == 9) {
-    tmem_alloc_pair(tmem_slot, 2 * NB);
+    tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
   }
   tc_fence_before();
@@ -603,7 +605,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
       uint32_t it = 0;
       bool ok = true;
       for (int tile = cluster; tile < ntiles && ok; tile += nclusters) {
-        const Int8Tile t = int8_pair_tile<NB>(tile, tiles_m, tiles_n);
+        const Int8Tile t = int8_pair_tile(tile, tiles_m, tiles_n);
         for (int kt = 0; kt < kts; ++kt, ++it) {
           const uint32_t s = it % kP8Stages;
           if (!mbar_wait(empty + s, ((it / kP8Stages) & 1u) ^ 1u, kDevErrTimeoutEmpty)) {
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
           unsigned char* sa = smem + s * kP8StageBytes;
           if (crank == 0) mbar_arrive_expect_tx(full + s, 2 * kP8StageBytes);
           tma_load_2d_pair(sa, &tm_x, full_even + 8 * s, kt * kI8KTile, t.m0 + 128 * (int)crank);
-          tma_load_2d_pair(sa + kI8StageA, &tm_w, full_even + 8 * s, kt * kI8KTile, t.n0 + NB / 2 * (int)crank);
+          tma_load_2d_pair(sa + kI8StageA, &tm_w, full_even + 8 * s, kt * kI8KTile, t.n0 + 128 * (int)crank);
         }
       }
       // After a failure, let this thread's loads land before the CTAs exit. The
@@ -627,7 +629,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
     }
   } else if (warp == 9) {
     if (lane == 0 && crank == 0) {
-      const uint32_t idesc = idesc_i8(256, NB);
+      const uint32_t idesc = idesc_i8(256, 256);
       const uint64_t dA0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
       const uint64_t dB0 = smem_desc(smem_u32(smem) + kI8StageA, 16, 1024, kSwizzle128B);
       uint32_t it = 0, tcount = 0;
@@ -649,7 +651,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
           const uint64_t off = (uint64_t)(s * ((uint32_t)kP8StageBytes >> 4));
 #pragma unroll
           for (int j = 0; j < kI8KTile / 32; ++j)
-            mma_i8_pair(tmem + NB * buf, dA0 + off + 2u * j, dB0 + off + 2u * j, idesc, (kt | j) != 0 ? 1u : 0u);
+            mma_i8_pair(tmem + 256 * buf, dA0 + off + 2u * j, dB0 + off + 2u * j, idesc, (kt | j) != 0 ? 1u : 0u);
           tc_commit_pair(empty + s, 0x3);
         }
         if (ok) tc_commit_pair(acc_full + buf, 0x3);
@@ -661,19 +663,19 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
     }
   } else {
     const int q = warp & 3, h = warp >> 2;
-    unsigned char* box = smem + C::kBoxOffset + warp * kP8BoxBytes;
-    float2* colv = reinterpret_cast<float2*>(smem + C::kColOffset) + warp * C::kCols;
+    unsigned char* box = smem + kP8BoxOffset + warp * kP8BoxBytes;
+    float2* colv = reinterpret_cast<float2*>(smem + kP8ColOffset) + warp * kP8Cols;
     const uint32_t acc_empty_even = mapa_shared(smem_u32(acc_empty), 0);
     constexpr int kBoxCols = 128 / (int)sizeof(OT);
     uint32_t tcount = 0;
     for (int tile = cluster; tile < ntiles; tile += nclusters, ++tcount) {
-      const Int8Tile t = int8_pair_tile<NB>(tile, tiles_m, tiles_n);
+      const Int8Tile t = int8_pair_tile(tile, tiles_m, tiles_n);
       const uint32_t buf = tcount & 1u;
-      const int m0 = t.m0 + 128 * (int)crank + 32 * q, n0 = t.n0 + C::kCols * h;
+      const int m0 = t.m0 + 128 * (int)crank + 32 * q, n0 = t.n0 + kP8Cols * h;
       const float sx = m0 + lane < a.M ? a.sx[m0 + lane] : 0.f;
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < C::kCols / 32; ++i) {
+      for (int i = 0; i < kP8Cols / 32; ++i) {
         const int n = n0 + 32 * i + lane;
         colv[32 * i + lane] = n < a.N ? make_float2(a.sw[n], a.bias ? a.bias[n] : 0.f) : make_float2(0.f, 0.f);
       }
@@ -682,10 +684,10 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
       ok = __all_sync(0xFFFFFFFFu, ok);
       tc_fence_after();
       if (!ok) break;
-      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + NB * buf + (uint32_t)(h * C::kCols);
+      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + 256 * buf + (uint32_t)(h * kP8Cols);
       const bool live = m0 < a.M;
 #pragma unroll
-      for (int b = 0; b < C::kCols / kBoxCols; ++b) {
+      for (int b = 0; b < kP8Cols / kBoxCols; ++b) {
         if (tma_y && lane == 0) bulk_wait_read<0>();   // the previous store from this box has read it
         __syncwarp();
 #pragma unroll
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
           uint32_t v[32];
           tmem_ld_32x32b_x32(taddr + b * kBoxCols + c, v);
           tmem_ld_wait();
-          if (b * kBoxCols + c + 32 == C::kCols) {   // the accumulator is drained
+          if (b * kBoxCols + c + 32 == kP8Cols) {   // the accumulator is drained
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
@@ -727,13 +729,17 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
         } else {
           __syncwarp();
           const int rows = min(32, a.M - m0);
-          for (int r = 0; r < rows; ++r)
+          OT* y = static_cast<OT*>(a.y) + (long long)m0 * a.ldy + col0;
 #pragma unroll
-            for (int c = 0; c < kBoxCols; c += 32) {
-              const int e = c + lane, byte = e * (int)sizeof(OT);
-              const OT value = *reinterpret_cast<const OT*>(box + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
-              if (col0 + e < a.N) static_cast<OT*>(a.y)[(long long)(m0 + r) * a.ldy + col0 + e] = value;
+          for (int c = 0; c < kBoxCols; c += 32) {
+            const int e = c + lane, byte = e * (int)sizeof(OT);
+            if (col0 + e < a.N) {
+#pragma unroll 8
+              for (int r = 0; r < rows; ++r)
+                y[r * a.ldy + e] = *reinterpret_cast<const OT*>(box + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
             }
+          }
+          __syncwarp();
         }
       }
     }
@@ -743,7 +749,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
   cluster_sync();   // no CTA leaves while its peer may still signal its barriers
   if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 2 * NB);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 

@@ -8,6 +8,7 @@ library is missing or the device is not sm_100, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -385,46 +386,52 @@ def svdq_deltaquant_encode(X: torch.Tensor, dims: tuple[int, int, int], out: tup
 # W8A8 linear, layer norm and rotary positions. Rows may have a stride; every
 # tensor of a call lives on one CUDA device, which need not be the current one.
 
+_FLOAT_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
 def _float_type(t: torch.Tensor, what: str) -> int:
-    if t.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+    code = _FLOAT_TYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{what} must be bf16, fp16 or fp32, not {t.dtype}")
-    return DTYPES[t.dtype]
+    return code
 
 
-def _device(X: torch.Tensor, *others: torch.Tensor | None) -> torch.device:
-    dev = X.device
-    if dev.type != "cuda":
+def _device(X: torch.Tensor, *others: torch.Tensor | None) -> int:
+    """Index of the CUDA device that holds all the tensors of a call."""
+    index = X.get_device()
+    if index < 0:
         raise ValueError("tensors must live on a CUDA device")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: all must live on one device")
-    return dev
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on {X.device} and {t.device}: all must live on one CUDA device")
+    return index
 
 
 def _rows(t: torch.Tensor, what: str) -> tuple[int, int]:
     """(address, row stride) of a matrix whose rows are contiguous."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    stride = t.stride()
+    if len(stride) != 2 or (stride[1] != 1 and t.shape[1] > 1):
         raise ValueError(f"{what} must be a matrix with contiguous rows")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), stride[0]
 
 
 def _dense(t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, what: str) -> int | None:
     """Address of a contiguous tensor of this shape and type (None: no tensor)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"not {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _call(dev: torch.device, fn, *args) -> None:
-    """fn(*args, stream) on dev's current stream, with dev current."""
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+def _call(index: int, fn, *args) -> None:
+    """fn(*args, stream) on the device's current stream, with the device current."""
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status:
         _check(status)
 
@@ -457,8 +464,8 @@ def svdq_int8_prepare_weights(W_lin: torch.Tensor, lam: torch.Tensor | None = No
         if bias.shape != (N,):
             raise ValueError(f"bias must have {N} values")
         bias = bias.float().contiguous()
-    Qw = torch.empty(N, K, dtype=torch.int8, device=dev)
-    Sw = torch.empty(N, dtype=torch.float32, device=dev)
+    Qw = W_lin.new_empty(N, K, dtype=torch.int8)
+    Sw = W_lin.new_empty(N, dtype=torch.float32)
     _call(dev, load().svdq_int8_quantize_weight, N, K, wt, wp, ldw, lp, Qw.data_ptr(), Sw.data_ptr())
     return Int8Weights(N, K, Qw, Sw, inv_lam, bias)
 
@@ -472,8 +479,8 @@ def svdq_int8_quantize_act(X: torch.Tensor, inv_lambda: torch.Tensor | None = No
     M, K = X.shape
     lp = _dense(inv_lambda, (K,), torch.float32, "inv_lambda")
     if out is None:
-        Qx = torch.empty(M, K, dtype=torch.int8, device=dev)
-        Sx = torch.empty(M, dtype=torch.float32, device=dev)
+        Qx = X.new_empty(M, K, dtype=torch.int8)
+        Sx = X.new_empty(M, dtype=torch.float32)
         qp, sp = Qx.data_ptr(), Sx.data_ptr()
     else:
         Qx, Sx = out
@@ -488,7 +495,7 @@ def svdq_int8_linear(Qx: torch.Tensor, Sx: torch.Tensor, W: Int8Weights, dtype: 
     """Y [M][N] = Sx Sw (Qx Qw^T) + bias of a W8A8 layer, in dtype (or out's: rows may be strided)."""
     dev = _device(Qx, Sx, W.Qw, W.Sw, W.bias, out)
     M, K, N = Qx.shape[0], W.K, W.N
-    Y = torch.empty(M, N, dtype=dtype, device=dev) if out is None else out
+    Y = Qx.new_empty(M, N, dtype=dtype) if out is None else out
     if Y.shape != (M, N):
         raise ValueError(f"out must be [{M}][{N}]")
     yt = _float_type(Y, "out")
@@ -543,7 +550,7 @@ def svdq_layernorm(X: torch.Tensor, weight: torch.Tensor | None = None, bias: to
     M, C = X.shape
     wt, wp, bp, rows, _ = _norm_params(X, weight, bias, rows_per_group)
     if out is None:
-        out = torch.empty(M, C, dtype=X.dtype, device=dev)
+        out = X.new_empty(M, C)
         yp, ldy = out.data_ptr(), C
     else:
         if out.shape != X.shape or out.dtype != X.dtype:
@@ -551,8 +558,8 @@ def svdq_layernorm(X: torch.Tensor, weight: torch.Tensor | None = None, bias: to
         yp, ldy = _rows(out, "out")
     mean = rstd = mp = rp = None
     if stats:
-        mean = torch.empty(M, dtype=torch.float32, device=dev)
-        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+        mean = X.new_empty(M, dtype=torch.float32)
+        rstd = X.new_empty(M, dtype=torch.float32)
         mp, rp = mean.data_ptr(), rstd.data_ptr()
     _call(dev, load().svdq_layernorm, M, C, xt, wt, xp, ldx, wp, bp, rows, eps, SVDQ_NORM_ADD_ONE if add_one else 0,
           yp, ldy, mp, rp)
@@ -572,7 +579,7 @@ def svdq_int8_layernorm_quantize(X: torch.Tensor, weight: torch.Tensor | None = 
     wt, wp, bp, rows, _ = _norm_params(X, weight, bias, rows_per_group)
     lp = _dense(inv_lambda, (C,), torch.float32, "inv_lambda")
     if out is None:
-        out = (torch.empty(M, C, dtype=torch.int8, device=dev), torch.empty(M, dtype=torch.float32, device=dev))
+        out = (X.new_empty(M, C, dtype=torch.int8), X.new_empty(M, dtype=torch.float32))
     Qx, Sx = out
     _device(X, Qx, Sx)
     _call(dev, load().svdq_int8_layernorm_quantize, M, C, xt, wt, xp, ldx, wp, bp, rows, eps,
@@ -585,6 +592,12 @@ def svdq_layernorm_backward_workspace(M: int, C: int, rows_per_group: int = 0) -
     v = ctypes.c_size_t()
     _check(load().svdq_layernorm_backward_workspace(M, C, rows_per_group, ctypes.byref(v)))
     return v.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _backward_workspace(index: int, M: int, C: int, rows_per_group: int) -> int:
+    with torch.cuda.device(index):
+        return svdq_layernorm_backward_workspace(M, C, rows_per_group)
 
 
 def svdq_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
@@ -602,7 +615,7 @@ def svdq_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Ten
     wt, wp, _, rows, groups = _norm_params(X, weight, None, rows_per_group)
     mp, rp = _dense(mean, (M,), torch.float32, "mean"), _dense(rstd, (M,), torch.float32, "rstd")
     if out is None:
-        out = torch.empty(M, C, dtype=X.dtype, device=dev)
+        out = X.new_empty(M, C)
         op, ldo = out.data_ptr(), C
     else:
         if out.shape != X.shape or out.dtype != X.dtype:
@@ -612,14 +625,13 @@ def svdq_layernorm_backward(dY: torch.Tensor, X: torch.Tensor, weight: torch.Ten
     ws = 0
     if params:
         shape = weight.shape if weight is not None else (C,) if groups == 1 else (groups, C)
-        new = torch.empty if M else torch.zeros
-        dw = new(shape, dtype=torch.float32, device=dev)
-        db = new(shape, dtype=torch.float32, device=dev)
+        new = X.new_empty if M else X.new_zeros
+        dw = new(shape, dtype=torch.float32)
+        db = new(shape, dtype=torch.float32)
         dwp, dbp = dw.data_ptr(), db.data_ptr()
-        with torch.cuda.device(dev):
-            ws = svdq_layernorm_backward_workspace(M, C, rows)
+        ws = _backward_workspace(dev, M, C, rows)
         if ws:
-            work = torch.empty(ws, dtype=torch.uint8, device=dev)
+            work = X.new_empty(ws, dtype=torch.uint8)
             kp = work.data_ptr()
     _call(dev, load().svdq_layernorm_backward, M, C, xt, wt, gp, ldg, xp, ldx, wp, mp, rp, rows,
           SVDQ_NORM_ADD_ONE if add_one else 0, op, ldo, dwp, dbp, kp, ws)
@@ -653,7 +665,8 @@ def svdq_rope(X: torch.Tensor, positions: torch.Tensor, table: RopeTable, interl
     a new contiguous tensor; out may be X."""
     dev = _device(X, positions, table.freqs, out)
     xt = _float_type(X, "X")
-    if X.dim() != 3 or X.stride(2) != 1:
+    x_stride = X.stride()
+    if len(x_stride) != 3 or x_stride[2] != 1:
         raise ValueError("X must be [T][heads][D] with contiguous heads")
     T, H, D = X.shape
     axes = len(table.axis_dims)
@@ -661,11 +674,12 @@ def svdq_rope(X: torch.Tensor, positions: torch.Tensor, table: RopeTable, interl
             positions.dtype not in (torch.int32, torch.float32):
         raise ValueError(f"positions must be a contiguous int32 or fp32 [P][{axes}] tensor")
     if out is None:
-        out = torch.empty(T, H, D, dtype=X.dtype, device=dev)
+        out = X.new_empty(T, H, D)
     elif out.shape != X.shape or out.dtype != X.dtype or out.stride(2) != 1:
         raise ValueError("out must have X's shape and type, and contiguous heads")
-    _call(dev, load().svdq_rope, T, H, D, xt, X.data_ptr(), X.stride(0), X.stride(1), out.data_ptr(), out.stride(0),
-          out.stride(1), positions.data_ptr(), DTYPES[positions.dtype], positions.shape[0], axes, table._dims,
+    y_stride = out.stride()
+    _call(dev, load().svdq_rope, T, H, D, xt, X.data_ptr(), x_stride[0], x_stride[1], out.data_ptr(), y_stride[0],
+          y_stride[1], positions.data_ptr(), DTYPES[positions.dtype], positions.shape[0], axes, table._dims,
           table.freqs.data_ptr(), (0 if interleaved else SVDQ_ROPE_HALVES) | (SVDQ_ROPE_INVERSE if inverse else 0))
     return out
 
