@@ -41,6 +41,9 @@ struct Tag {
   using type = T;
 };
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
 template <auto K>
 struct Kern {
   static constexpr auto value = K;
@@ -85,16 +88,19 @@ int ring_blocks_per_sm(int threads, size_t smem) {
   return std::max(n, 1);
 }
 
-// Launches a ring kernel that takes rows in turn, `elems` elements a thread.
-template <auto KERN, typename Args>
+// Launches a ring kernel that takes rows in turn, `elems` elements a thread;
+// FULL_KERN where the columns fill whole warps.
+template <auto KERN, auto FULL_KERN, typename Args>
 svdq_status launch_rows(Args a, int64_t rows, int64_t cols, int elems, size_t row_bytes, cudaStream_t st) {
+  const auto kern = cols % (32 * elems) == 0 ? FULL_KERN : KERN;
   const int threads = round_up((int)((cols + elems - 1) / elems), 32);
   a.depth = ring_depth(threads, row_bytes);
   const size_t smem = a.depth * row_bytes;
-  const int64_t blocks = (int64_t)sm_count() * ring_blocks_per_sm<KERN>(threads, smem);
+  const int64_t blocks = (int64_t)sm_count() *
+                         (kern == FULL_KERN ? ring_blocks_per_sm<FULL_KERN>(threads, smem) : ring_blocks_per_sm<KERN>(threads, smem));
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = pdl_config((unsigned)std::min<int64_t>(rows, blocks), threads, smem, st, attr);
-  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, KERN, a));
+  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
   return SVDQ_OK;
 }
 
@@ -144,11 +150,15 @@ svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_
     }
     if (K <= 16384 && M > 2 * sms) {
       using namespace svdq;
-      const size_t row = (size_t)K * sizeof(T);
-      if (K <= 2048) return launch_rows<int8_quantize_rows_kernel<T, 16, 4>>(a, M, K, 16, row, st);
-      if (K <= 4096) return launch_rows<int8_quantize_rows_kernel<T, 32, 4>>(a, M, K, 32, row, st);
-      if (K <= 8192) return launch_rows<int8_quantize_rows_kernel<T, 32, 8>>(a, M, K, 32, row, st);
-      return launch_rows<int8_quantize_rows_kernel<T, 32, 16>>(a, M, K, 32, row, st);
+      auto go = [&](auto elems, auto warps) -> svdq_status {
+        constexpr int E = decltype(elems)::value, W = decltype(warps)::value;
+        return launch_rows<int8_quantize_rows_kernel<T, E, W, false>, int8_quantize_rows_kernel<T, E, W, true>>(
+            a, M, K, E, (size_t)K * sizeof(T), st);
+      };
+      if (K <= 2048) return go(Int<16>(), Int<4>());
+      if (K <= 4096) return go(Int<32>(), Int<4>());
+      if (K <= 8192) return go(Int<32>(), Int<8>());
+      return go(Int<32>(), Int<16>());
     }
     const unsigned grid = (unsigned)std::min<int64_t>(M, sms * 8);
     if (vecs <= 512) return launch_int8_quantize<T, 2, 256>(a, grid, round_up((vecs + 1) / 2, 32), st);
@@ -410,10 +420,15 @@ svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStr
       if (n.C > 512 && n.M > 2 * sm_count()) {
         using namespace svdq;
         const size_t row = (size_t)n.C * sizeof(T);
-        if (n.C <= 2048) return launch_rows<layernorm_rows_kernel<T, WT, 16, 4, QUANT>>(a, n.M, n.C, 16, row, st);
-        if (n.C <= 4096) return launch_rows<layernorm_rows_kernel<T, WT, 32, 4, QUANT>>(a, n.M, n.C, 32, row, st);
-        if (n.C <= 8192) return launch_rows<layernorm_rows_kernel<T, WT, 32, 8, QUANT>>(a, n.M, n.C, 32, row, st);
-        return launch_rows<layernorm_rows_kernel<T, WT, 32, 16, QUANT>>(a, n.M, n.C, 32, row, st);
+        auto go = [&](auto elems, auto warps) -> svdq_status {
+          constexpr int E = decltype(elems)::value, W = decltype(warps)::value;
+          return launch_rows<layernorm_rows_kernel<T, WT, E, W, QUANT, false>,
+                             layernorm_rows_kernel<T, WT, E, W, QUANT, true>>(a, n.M, n.C, E, row, st);
+        };
+        if (n.C <= 2048) return go(Int<16>(), Int<4>());
+        if (n.C <= 4096) return go(Int<32>(), Int<4>());
+        if (n.C <= 8192) return go(Int<32>(), Int<8>());
+        return go(Int<32>(), Int<16>());
       }
     }
     return norm_width<VEC>(pieces, [&](auto nv, auto maxt) -> svdq_status {
@@ -612,9 +627,11 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
       if (n.C > 512) {
         using namespace svdq;
         const size_t rows = 2 * (size_t)n.C * sizeof(T);
-        auto go = [&](auto kern_c, int elems) -> svdq_status {
-          constexpr auto kern = decltype(kern_c)::value;
-          const int threads = round_up(((int)n.C + elems - 1) / elems, 32);
+        auto go = [&](auto elems, auto warps, auto blocks, auto hold, auto full) -> svdq_status {
+          constexpr int E = decltype(elems)::value;
+          constexpr auto kern = layernorm_backward_rows_kernel<T, WT, E, decltype(warps)::value, decltype(blocks)::value,
+                                                               decltype(hold)::value, decltype(full)::value>;
+          const int threads = round_up(((int)n.C + E - 1) / E, 32);
           a.depth = ring_depth(threads, rows, (size_t)n.C * 4);
           const size_t smem = a.depth * rows + (size_t)n.C * 4;
           ring_blocks_per_sm<kern>(threads, smem);   // sets the attribute
@@ -623,9 +640,13 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
           SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
           return SVDQ_OK;
         };
-        if (n.C <= 5120) return go(Kern<layernorm_backward_rows_kernel<T, WT, 16, 10, 2, true>>(), 16);
-        if (n.C <= 8192) return go(Kern<layernorm_backward_rows_kernel<T, WT, 16, 16, 1, true>>(), 16);
-        return go(Kern<layernorm_backward_rows_kernel<T, WT, 32, 16, 1, false>>(), 32);
+        auto size = [&](auto elems, auto warps, auto blocks, auto hold) -> svdq_status {
+          if (n.C % (32 * decltype(elems)::value) == 0) return go(elems, warps, blocks, hold, std::true_type());
+          return go(elems, warps, blocks, hold, std::false_type());
+        };
+        if (n.C <= 5120) return size(Int<16>(), Int<10>(), Int<2>(), std::true_type());
+        if (n.C <= 8192) return size(Int<16>(), Int<16>(), Int<1>(), std::true_type());
+        return size(Int<32>(), Int<16>(), Int<1>(), std::false_type());
       }
     }
     return norm_width<VEC>(pieces, [&](auto nv, auto maxt) -> svdq_status {

@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(MAXT, 1) int8_quantize_kernel(const Int8QuantA
 }
 
 // Many rows of more than one warp: a block per row, rows streamed through the
-// ring, the factors in registers, E elements a thread.
-template <typename T, int E, int W>
+// ring, the factors in registers, E elements a thread; FULL: K fills them all.
+template <typename T, int E, int W, bool FULL>
 __global__ void __launch_bounds__(32 * W, 16 / W) int8_quantize_rows_kernel(const Int8QuantArgs a) {
   constexpr int N = kVecN<T>, NV = E / N, H = N / 2;
   extern __shared__ __align__(16) unsigned char quant_ring[];
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) int8_quantize_rows_kernel(cons
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int k = (v * (int)blockDim.x + tid) * N;
-    in[v] = k < a.K;
+    in[v] = FULL || k < a.K;
 #pragma unroll
     for (int i = 0; i < H; ++i) l[v][i] = pair(1.f);
     if (a.mult && in[v]) load_pairs<float, N>(a.mult + k, l[v]);

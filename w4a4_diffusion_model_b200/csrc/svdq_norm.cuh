@@ -168,10 +168,12 @@ __device__ __forceinline__ float4 warp_moments(float sum, float sq, float2 n) {
 // elements (the wait, shuffles, the join) is shared by more. W: warps the block
 // may have; the join runs over all of them, unrolled (absent ones hold zeros).
 //
-// Mean and variance take one barrier: each warp forms its own mean and its own
-// sum of squares around that mean, and every thread joins the warps',
-//   M2 = sum_w (M2_w + n_w (mean_w - mean)^2).
-template <typename T, typename WT, int E, int W, bool QUANT>
+// Mean and variance take one barrier: each thread forms its own mean and its sum
+// of squares around that, a warp joins its threads' and every thread joins the
+// warps', each time by
+//   M2 = sum_i (M2_i + n_i (mean_i - mean)^2).
+// FULL: the row fills every piece of every thread.
+template <typename T, typename WT, int E, int W, bool QUANT, bool FULL>
 __global__ void __launch_bounds__(32 * W, 16 / W) layernorm_rows_kernel(const NormArgs a) {
   constexpr int N = kVecN<T>, NV = E / N, H = N / 2;
   extern __shared__ __align__(16) unsigned char norm_ring[];
@@ -193,11 +195,12 @@ __global__ void __launch_bounds__(32 * W, 16 / W) layernorm_rows_kernel(const No
   int mine = 0;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    in[v] = (v * (int)blockDim.x + tid) * N < a.C;
+    in[v] = FULL || (v * (int)blockDim.x + tid) * N < a.C;
     mine += in[v] ? N : 0;
   }
-  mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-  const float n = (float)mine, inv_n = mine ? 1.f / (float)mine : 0.f;   // elements of this warp
+  const int warp_has = __reduce_add_sync(0xFFFFFFFFu, mine);
+  const float own_n = (float)mine, inv_own = mine ? 1.f / (float)mine : 0.f;          // elements of this thread
+  const float n = (float)warp_has, inv_n = warp_has ? 1.f / (float)warp_has : 0.f;   // and of this warp
   __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
@@ -243,19 +246,22 @@ __global__ void __launch_bounds__(32 * W, 16 / W) layernorm_rows_kernel(const No
 #pragma unroll
       for (int i = 0; i < H; ++i) sum2 = add2_rn(sum2, f[v][i]);
     }
-    const float sum = warp_sum(sum2.x + sum2.y);
-    const float own = sum * inv_n;
+    // around the thread's own mean first: this sweep does not wait for a shuffle
+    const float mine_sum = sum2.x + sum2.y, mine_mean = mine_sum * inv_own;
     float2 sq2 = pair(0.f);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
       if (in[v]) {
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-          const float2 d = add2_rn(f[v][i], pair(-own));
+          const float2 d = add2_rn(f[v][i], pair(-mine_mean));
           sq2 = fma2_rn(d, d, sq2);
         }
       }
-    const float sq = warp_sum(sq2.x + sq2.y);
+    const float sum = warp_sum(mine_sum);
+    const float own = sum * inv_n;
+    const float off = mine_mean - own;
+    const float sq = warp_sum(fmaf(own_n * off, off, sq2.x + sq2.y));
     if (lane == 0) moments[turn][warp] = make_float4(sum, sq, n, own);
     __syncthreads();
     if (tid == 0 && m < M - ahead) ring.fetch(stage, m + ahead);
@@ -459,8 +465,8 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormA
 // columns: it is read back once a row, and its registers are worth more to a
 // second resident block). HOLD: xhat and h stay in registers between the row's
 // two sweeps; else (E = 32, rows of more than 8192) the second sweep forms them
-// again from the stage, which then waits for one more barrier.
-template <typename T, typename WT, int E, int W, int BLOCKS, bool HOLD>
+// again from the stage, which then waits for one more barrier. FULL as above.
+template <typename T, typename WT, int E, int W, int BLOCKS, bool HOLD, bool FULL>
 __global__ void __launch_bounds__(32 * W, BLOCKS) layernorm_backward_rows_kernel(const NormArgs a) {
   constexpr int N = kVecN<T>, NV = E / N, H = N / 2;
   extern __shared__ __align__(16) unsigned char norm_ring[];
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(32 * W, BLOCKS) layernorm_backward_rows_kernel
   float2 dw[NV][H], db[NV][H];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    in[v] = (v * (int)blockDim.x + tid) * N < a.C;
+    in[v] = FULL || (v * (int)blockDim.x + tid) * N < a.C;
 #pragma unroll
     for (int i = 0; i < H; ++i) dw[v][i] = db[v][i] = pair(0.f);
   }
