@@ -49,6 +49,8 @@ struct NormArgs {
   float* part;           // [chunks][2][groups][C] partial sums of dw and db, null: one chunk, straight to dw and db
   int chunks;            // row chunks per group
   int depth;             // stages of the row ring
+  int strip_blocks;      // few rows: blocks that sum columns, ahead of those that form dx
+  int first_block;       // few rows: number of the launch's first block
 };
 
 template <typename WT, int N>
@@ -461,9 +463,9 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormA
 
 // Backward for rows of more than one warp: a block per chunk of a group's rows,
 // rows of x and dy streamed through the ring, the chunk's dw and db in
-// registers (2 E of them), the weight in shared memory (each thread its own
-// columns: it is read back once a row, and its registers are worth more to a
-// second resident block). HOLD: xhat and h stay in registers between the row's
+// registers (2 E of them). The weight is in registers too where two blocks of 8
+// warps fit beside each other with it, else in shared memory (each thread its own
+// columns, read back once a row). HOLD: xhat and h stay in registers between the row's
 // two sweeps; else (E = 32, rows of more than 8192) the second sweep forms them
 // again from the stage, which then waits for one more barrier. FULL as above.
 template <typename T, typename WT, int E, int W, int BLOCKS, bool HOLD, bool FULL>
@@ -478,7 +480,9 @@ __global__ void __launch_bounds__(32 * W, BLOCKS) layernorm_backward_rows_kernel
   RowRing<2> ring = {norm_ring, full,
                      {static_cast<const unsigned char*>(a.x), static_cast<const unsigned char*>(a.dy)},
                      {a.ldx * (long long)sizeof(T), a.lddy * (long long)sizeof(T)}, row_bytes, a.depth};
+  constexpr bool kGainRegs = HOLD && W <= 8;
   float* gain = reinterpret_cast<float*>(norm_ring + 2 * (size_t)a.depth * row_bytes);   // [C]
+  float2 gr[kGainRegs ? NV : 1][H];
   if (tid == 0) ring.init();
   if (tid < 2 * W) (&slots[0][0])[tid] = pair(0.f);
   const long long g = blockIdx.x / a.chunks, groups = gridDim.x / a.chunks;
@@ -508,7 +512,14 @@ __global__ void __launch_bounds__(32 * W, BLOCKS) layernorm_backward_rows_kernel
       float w[N];
       norm_gain<WT, N>(a, g, c, w);
 #pragma unroll
-      for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(gain + c + i) = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+      for (int i = 0; i < N; i += 4) {
+        if constexpr (kGainRegs) {
+          gr[v][i / 2] = make_float2(w[i], w[i + 1]);
+          gr[v][i / 2 + 1] = make_float2(w[i + 2], w[i + 3]);
+        } else {
+          *reinterpret_cast<float4*>(gain + c + i) = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        }
+      }
     }
   int stage = 0, turn = 0;
   uint32_t parity = 0;
@@ -534,9 +545,14 @@ __global__ void __launch_bounds__(32 * W, BLOCKS) layernorm_backward_rows_kernel
       unpack_pairs<T>(*reinterpret_cast<const uint4*>(at + row_bytes), dy);
 #pragma unroll
       for (int i = 0; i < H; i += 2) {
-        const float4 w = *reinterpret_cast<const float4*>(gain + (v * (int)blockDim.x + tid) * N + 2 * i);
-        h[i] = mul2_rn(dy[i], make_float2(w.x, w.y));
-        h[i + 1] = mul2_rn(dy[i + 1], make_float2(w.z, w.w));
+        if constexpr (kGainRegs) {
+          h[i] = mul2_rn(dy[i], gr[v][i]);
+          h[i + 1] = mul2_rn(dy[i + 1], gr[v][i + 1]);
+        } else {
+          const float4 w = *reinterpret_cast<const float4*>(gain + (v * (int)blockDim.x + tid) * N + 2 * i);
+          h[i] = mul2_rn(dy[i], make_float2(w.x, w.y));
+          h[i + 1] = mul2_rn(dy[i + 1], make_float2(w.z, w.w));
+        }
       }
 #pragma unroll
       for (int i = 0; i < H; ++i) xh[i] = mul2_rn(add2_rn(xh[i], pair(-mean)), pair(rstd));
@@ -610,6 +626,96 @@ __global__ void __launch_bounds__(32 * W, BLOCKS) layernorm_backward_rows_kernel
         if (pb) *reinterpret_cast<float4*>(pb + c + 2 * i) = make_float4(db[v][i].x, db[v][i].y, db[v][i + 1].x, db[v][i + 1].y);
       }
     }
+}
+
+// Backward for few rows, in one launch: dw and db need no reduction over a row
+// (the statistics are given), so the first strip_blocks blocks each sum a strip
+// of 32 columns over a group's rows, a warp every 16th row, while the others form
+// dx. Both read x and dy, from L2 the second time, which is what few rows cost;
+// nothing is kept in between. A row's dx takes a warp up to 1024 channels, else
+// the block.
+constexpr int kNormFewThreads = 512;
+
+template <typename T, typename WT, bool VEC>
+__global__ void __launch_bounds__(kNormFewThreads) layernorm_backward_few_kernel(const NormArgs a) {
+  using P = Piece<T, VEC>;
+  constexpr int N = P::kN, kWarps = kNormFewThreads / 32;
+  __shared__ float sums[2][kWarps][33];
+  __shared__ float2 slot[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int block = (int)blockIdx.x + a.first_block;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (block < a.strip_blocks) {
+    const int strips = (a.C + 31) / 32;
+    const long long g = block / strips;
+    const int c = (block % strips) * 32 + lane;
+    const long long row0 = g * a.rows_per_group;
+    const int rows = (int)min(a.rows_per_group, a.M - row0);
+    float w = 0.f, b = 0.f;
+    if (c < a.C) {
+      const T* x = static_cast<const T*>(a.x) + row0 * a.ldx + c;
+      const T* dy = static_cast<const T*>(a.dy) + row0 * a.lddy + c;
+#pragma unroll 8
+      for (int r = warp; r < rows; r += kWarps) {
+        const float d = to_float(dy[r * a.lddy]);
+        w = fmaf(d, (to_float(x[r * a.ldx]) - a.mean[row0 + r]) * a.rstd[row0 + r], w);
+        b += d;
+      }
+    }
+    sums[0][warp][lane] = w;
+    sums[1][warp][lane] = b;
+    __syncthreads();
+    if (warp < 2 && c < a.C) {
+      float t = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) t += sums[warp][k][lane];
+      float* out = warp ? a.db : a.dw;
+      if (out) out[g * a.C + c] = t;
+    }
+    return;
+  }
+  const bool narrow = a.C <= 1024;
+  const int tid = narrow ? lane : (int)threadIdx.x, team = narrow ? 32 : kNormFewThreads;
+  const long long m = narrow ? (long long)(block - a.strip_blocks) * kWarps + warp : block - a.strip_blocks;
+  if (m >= a.M) return;                       // a warp of its own, or no block at all
+  const long long g = m / a.rows_per_group;
+  const T* x = static_cast<const T*>(a.x) + m * a.ldx;
+  const T* dy = static_cast<const T*>(a.dy) + m * a.lddy;
+  const float mean = a.mean[m], rstd = a.rstd[m];
+  auto piece = [&](int c, float (&xh)[N], float (&h)[N]) {
+    float w[N];
+    P::unpack(P::load(x + c), xh);
+    P::unpack(P::load(dy + c), h);
+    norm_gain<WT, N>(a, g, c, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      xh[i] = (xh[i] - mean) * rstd;
+      h[i] *= w[i];
+    }
+  };
+  float s1 = 0.f, s2 = 0.f;
+#pragma unroll 4
+  for (int c = tid * N; c < a.C; c += team * N) {
+    float xh[N], h[N];
+    piece(c, xh, h);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      s1 += h[i];
+      s2 = fmaf(h[i], xh[i], s2);
+    }
+  }
+  const float2 s = team_sum2(s1, s2, team / 32, slot);
+  const float m1 = s.x / (float)a.C, m2 = s.y / (float)a.C;
+  T* dx = static_cast<T*>(a.dx) + m * a.lddx;
+#pragma unroll 4
+  for (int c = tid * N; c < a.C; c += team * N) {
+    float xh[N], h[N];
+    piece(c, xh, h);
+#pragma unroll
+    for (int i = 0; i < N; ++i) h[i] = rstd * (h[i] - m1 - xh[i] * m2);
+    P::store(dx + c, h);
+  }
 }
 
 // dw and db from the chunks' partial rows: a block takes 32 columns, its warp
