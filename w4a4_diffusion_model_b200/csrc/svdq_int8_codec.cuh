@@ -4,14 +4,17 @@
 // holds an infinity or a NaN gets the scale NaN and codes 0, so that what is
 // computed from it is NaN.
 //
-// The quotient is taken as v * fp32(1/s), which is off the exact one by at most
-// 127 * 2^-23 < 2^-16. Where it lands within 2^-15 of a midpoint (one value in
-// 16000) the code is settled exactly: with the candidate q, e = v - q s comes
-// from one fused multiply-add, and 2|e| against s decides. For q = 0 and
-// |q| >= 2 that e is exact (v and q s are multiples of ulp(s), |e| is near
-// s / 2 and has at most 24 bits). For |q| = 1 a v just below s / 2 can need 25
-// bits; then |e| > s / 2 rounds to s / 2 at the least, which an odd q treats
-// alike.
+// The quotient is taken as v * fp32(1/s), its product rounded only with the sum
+// that makes an integer of it, so it is off the exact one by at most
+// 127 * 2^-24 < 2^-17. Pieces in which one lands within 2^-16 of a midpoint are
+// settled exactly: with the candidate q, e = v - q s comes from one fused
+// multiply-add, and 2|e| against s decides. For q = 0 and |q| >= 2 that e is
+// exact (v and q s are multiples of ulp(s), |e| is near s / 2 and has at most 24
+// bits). For |q| = 1 a v just below s / 2 can need 25 bits; then |e| > s / 2
+// rounds to s / 2 at the least, which an odd q treats alike. Settling is no rare
+// case: 16-bit values over their own maximum are ratios of small integers, and in
+// rows whose maximum has a short significand many of 127 v / max fall on a
+// midpoint (all 256 values of a warp's piece are settled when one of them does).
 #pragma once
 
 #include <cstdint>
@@ -21,51 +24,56 @@
 namespace svdq {
 
 struct Int8Scale {
-  float s;       // what is stored
-  float rcp;     // fp32(1/s); 0: codes 0, or
-  bool small;    // s is too small for the quick quotient
+  float s;        // what is stored
+  float rcp;      // fp32(1/s); 0: codes 0
+  bool special;   // the row is not finite, or s too small for fp32 quotients
 };
 
 __device__ __forceinline__ Int8Scale int8_scale(float amax) {
+  if (!(amax <= 3.4028235e38f)) return Int8Scale{__int_as_float(0x7FC00000), 0.f, true};
   Int8Scale r;
-  if (!(amax <= 3.4028235e38f)) return Int8Scale{__int_as_float(0x7FC00000), 0.f, false};
   r.s = __fdiv_rn(amax, 127.f);
-  r.small = r.s < 1e-30f && r.s > 0.f;
-  r.rcp = r.s > 0.f && !r.small ? __frcp_rn(r.s) : 0.f;
+  r.special = r.s < 1e-30f && r.s > 0.f;
+  r.rcp = r.s >= 1e-30f ? __frcp_rn(r.s) : 0.f;
   return r;
 }
 
-// The code of v from the candidate q, |q - v/s| < 1.
-__device__ __forceinline__ float int8_settle(float v, float q, float s) {
-  const float e = fmaf(-q, s, v), d = fabsf(e) + fabsf(e);
-  const bool odd = (__float2int_rn(q) & 1) != 0;
-  if (d > s || (d == s && odd)) q += e > 0.f ? 1.f : -1.f;
-  return q;
-}
-
-// Codes of v for scales too small for fp32 products: the quotient of two fp32
-// values differs from a midpoint by more than 2^-34, or is one, so fp64
-// rounds it right.
-__device__ __forceinline__ float int8_code_small(float v, float s) {
-  const double q = rint((double)v / (double)s);
-  return (float)fmin(fmax(q, -127.0), 127.0);
-}
-
 constexpr float kInt8Magic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer, left in the low bits
+constexpr float kInt8Near = 0.5f - 0x1p-16f;
 
 // Candidate codes of two values, still carrying kInt8Magic; `far` collects how
 // far the quotients are from them.
-__device__ __forceinline__ float2 int8_quick(float2 v, const Int8Scale& sc, float& far) {
-  const float2 r = make_float2(sc.rcp, sc.rcp), magic = make_float2(kInt8Magic, kInt8Magic);
+__device__ __forceinline__ float2 int8_quick(float2 v, float rcp, float& far) {
+  const float2 r = make_float2(rcp, rcp), magic = make_float2(kInt8Magic, kInt8Magic);
   const float2 b = fma2_rn(v, r, magic);
   const float2 d = fma2_rn(v, r, fma2_rn(b, make_float2(-1.f, -1.f), magic));
   asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(far) : "f"(far), "f"(d.x), "f"(d.y));
   return b;
 }
 
-__device__ __forceinline__ float int8_careful(float v, float b, const Int8Scale& sc) {
-  if (sc.rcp == 0.f) return (sc.small ? int8_code_small(v, sc.s) : 0.f) + kInt8Magic;
-  return int8_settle(v, b - kInt8Magic, sc.s) + kInt8Magic;
+// One step from candidate b towards v where 2|e| > s, or where they are equal
+// and the code is odd (b's last bit): d = 2|e| - s as an integer is then positive
+// with that bit added.
+__device__ __forceinline__ float int8_step(float b, float e, float s) {
+  const float d = fmaf(2.f, fabsf(e), -s);
+  return __float_as_int(d) + (__float_as_int(b) & 1) > 0 ? b + copysignf(1.f, e) : b;
+}
+
+__device__ __forceinline__ float2 int8_settle(float2 v, float2 b, float s) {
+  const float2 q = fma2_rn(b, make_float2(-1.f, -1.f), make_float2(kInt8Magic, kInt8Magic));   // -q
+  const float2 e = fma2_rn(q, make_float2(s, s), v);
+  return make_float2(int8_step(b.x, e.x, s), int8_step(b.y, e.y, s));
+}
+
+// Codes of a special row: 0 where it is not finite; else v and s are brought
+// into range by 2^100, and the code is clamped (s has so few bits that max / s
+// can pass 127).
+__device__ __noinline__ float2 int8_special(float2 v, float s) {
+  if (!(s < 1.f)) return make_float2(kInt8Magic, kInt8Magic);
+  const float k = 0x1p100f, t = s * k;
+  float far = 0.f;
+  v = make_float2(fminf(fmaxf(v.x * k, -127.f * t), 127.f * t), fminf(fmaxf(v.y * k, -127.f * t), 127.f * t));
+  return int8_settle(v, int8_quick(v, __frcp_rn(t), far), t);
 }
 
 // N = 4 or 8 consecutive codes (the address is a multiple of N).
@@ -74,10 +82,14 @@ __device__ __forceinline__ void int8_store(int8_t* out, const float2 (&v)[N / 2]
   float2 b[N / 2];
   float far = 0.f;
 #pragma unroll
-  for (int i = 0; i < N / 2; ++i) b[i] = int8_quick(v[i], sc, far);
-  if (far > 0.5f - 0x1p-15f || sc.rcp == 0.f) {
+  for (int i = 0; i < N / 2; ++i) b[i] = int8_quick(v[i], sc.rcp, far);
+  if (far > kInt8Near) {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) b[i] = make_float2(int8_careful(v[i].x, b[i].x, sc), int8_careful(v[i].y, b[i].y, sc));
+    for (int i = 0; i < N / 2; ++i) b[i] = int8_settle(v[i], b[i], sc.s);
+  }
+  if (sc.special) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) b[i] = int8_special(v[i], sc.s);
   }
   uint32_t w[N / 4];
 #pragma unroll
@@ -94,10 +106,12 @@ __device__ __forceinline__ void int8_store(int8_t* out, const float2 (&v)[N / 2]
 template <int N>
 __device__ __forceinline__ void int8_store(int8_t* out, const float (&v)[N], const Int8Scale& sc) {
   if constexpr (N == 1) {
+    const float2 one = make_float2(v[0], 0.f);
     float far = 0.f;
-    float b = int8_quick(make_float2(v[0], 0.f), sc, far).x;
-    if (far > 0.5f - 0x1p-15f || sc.rcp == 0.f) b = int8_careful(v[0], b, sc);
-    out[0] = (int8_t)(__float_as_uint(b) & 0xFFu);
+    float2 b = int8_quick(one, sc.rcp, far);
+    if (far > kInt8Near) b = int8_settle(one, b, sc.s);
+    if (sc.special) b = int8_special(one, sc.s);
+    out[0] = (int8_t)(__float_as_uint(b.x) & 0xFFu);
   } else {
     float2 p[N / 2];
 #pragma unroll
