@@ -110,11 +110,49 @@ def test_product(M, K, N, dtype):
     check_product(M, K, N, dtype, bias=(M + N) % 2 == 0)
 
 
+# each kernel and K split, as their sizes choose them: dot products for 1, 2, 4 and 8 tokens; a single CTA's tile with K
+# whole, in halves and in quarters; pairs whole and in halves; each with whole and ragged rows, columns and K
+@pytest.mark.parametrize("M,K,N", [(1, 1040, 520), (2, 528, 1001), (3, 2064, 300), (7, 4112, 1030),
+                                   (16, 4096, 24600), (40, 1360, 24577), (16, 4096, 12288), (13, 4112, 12289),
+                                   (100, 4096, 4096), (77, 4240, 2050), (1024, 1024, 2048), (700, 1104, 4097),
+                                   (1024, 8192, 1024), (1100, 8208, 1033)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_every_route(M, K, N, dtype):
+    check_product(M, K, N, dtype, bias=True, seed=5)
+
+
 @pytest.mark.parametrize("M,K,N", [(5, 64, 40), (300, 256, 512), (130, 320, 136)])
 @pytest.mark.parametrize("extra", [1, 4, 8])
 def test_product_into_wider_rows(M, K, N, extra):
     for dtype in TYPES:
         check_product(M, K, N, dtype, True, stride=N + extra)
+
+
+def test_unsmoothed_rows_whose_quotients_are_midpoints():
+    """16-bit rows over maxima with short significands: 127 x / max is half an integer for many x."""
+    g = torch.Generator().manual_seed(2)
+    for dtype in TYPES[:2]:
+        x = torch.randn(64, 1024, generator=g)
+        top = torch.tensor([4.0, 3.9375, 3.96875, 3.0, 2.5, 127.0, 63.5, 254.0]).repeat(8)
+        x = torch.minimum(torch.maximum(x, -top[:, None]), top[:, None])
+        x[:, 0] = top
+        x[32:, 1:] *= (top[32:] / 4)[:, None]
+        x = x.to(dtype)
+        Q, s = S.svdq_int8_quantize_act(x.cuda())
+        check_codes(x, None, Q, s)
+
+
+def test_many_rows_take_the_ring():
+    """More rows than two per SM: rows streamed through shared memory, whole and ragged widths, strided."""
+    for K in (528, 1024, 2064, 4096, 5136, 8192, 13824, 16384):
+        M = 700 if K <= 4096 else 400
+        x = activations(M, K + 16, torch.bfloat16, K)
+        mult = torch.exp(torch.randn(K, generator=torch.Generator().manual_seed(K)))
+        Q, s = S.svdq_int8_quantize_act(x.cuda()[:, 16:], mult.cuda())
+        check_codes(x[:, 16:], mult, Q, s)
+    x = activations(500, 1040, torch.float32, 9)
+    Q, s = S.svdq_int8_quantize_act(x.cuda())
+    check_codes(x, None, Q, s)
 
 
 def test_extreme_codes_sum_exactly():
@@ -172,6 +210,26 @@ def test_guards_around_every_output(M, K, N):
     S.svdq_check()
     for b in (qb, sb, yb):
         assert (b[:4096] == 0xA5).all() and (b[-4096:] == 0xA5).all()
+
+
+def test_weights_quantized_on_the_stream_just_before():
+    """The product follows the weights' quantizer on the stream with nothing in between, many times."""
+    g = torch.Generator().manual_seed(12)
+    for M, K, N in ((1, 1024, 512), (4, 4096, 2048), (32, 2048, 2048), (300, 512, 1024)):
+        q = torch.randint(-127, 128, (M, K), generator=g, dtype=torch.int8).cuda()
+        sx = torch.ones(M).cuda()
+        ws = [torch.randn(N, K, generator=g).cuda() for _ in range(3)]
+        prepared = [S.svdq_int8_prepare_weights(w) for w in ws]
+        torch.cuda.synchronize()
+        want = [S.svdq_int8_linear(q, sx, P) for P in prepared]
+        torch.cuda.synchronize()
+        W = prepared[0]
+        for _ in range(4):
+            for w, y in zip(ws, want):
+                lib = S.load()
+                st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+                assert lib.svdq_int8_quantize_weight(N, K, 2, w.data_ptr(), K, None, W.Qw.data_ptr(), W.Sw.data_ptr(), st) == 0
+                assert torch.equal(S.svdq_int8_linear(q, sx, W), y)
 
 
 def test_replayed_graph_and_other_stream():

@@ -115,6 +115,40 @@ def test_strided_rows_and_in_place(C, pad):
     assert torch.equal(X, Y) and (wide[:, C:] == 5).all() and (grad[:, C:] == 5).all()
 
 
+# more rows than two per SM: rows streamed through the ring, in each of its widths, whole and ragged
+@pytest.mark.parametrize("C", [520, 1024, 2048, 2056, 4096, 4104, 5120, 8192, 12288, 16384])
+def test_many_rows(C):
+    M = 600 if C <= 5120 else 310
+    for dtype, wtype, groups in ((BF, BF, 2), (FP32, FP32, None)):
+        run(*case(M, C, dtype, wtype, groups), add_one=groups is not None)
+
+
+def test_many_groups_of_many_rows():
+    run(*case(1200, 1024, BF, FP32, 240))
+    run(*case(1203, 640, FP16, FP16, 241), rows=5)
+
+
+@pytest.mark.parametrize("M,C", [(40, 96), (700, 96), (200, 1160), (700, 1160), (340, 9000)])
+def test_gradient_in_the_memory_of_either_input(M, C):
+    x, w, b, dy = (t.cuda() for t in case(M, C, BF, BF, None))
+    _, mean, rstd = S.svdq_layernorm(x, w, b)
+    want = S.svdq_layernorm_backward(dy, x, w, mean, rstd)
+    for which in (0, 1):
+        a = [dy.clone(), x.clone()]
+        got = S.svdq_layernorm_backward(a[0], a[1], w, mean, rstd, out=a[which])
+        for p, q in zip(want, got):
+            assert torch.equal(p, q)
+
+
+def test_only_the_gradient_of_the_input():
+    for M in (40, 800):
+        x, w, b, dy = (t.cuda() for t in case(M, 200, BF, BF, None))
+        _, mean, rstd = S.svdq_layernorm(x, w, b)
+        want = S.svdq_layernorm_backward(dy, x, w, mean, rstd)
+        dX, dw, db = S.svdq_layernorm_backward(dy, x, w, mean, rstd, params=False)
+        assert torch.equal(dX, want[0]) and dw is None and db is None
+
+
 def test_no_rows():
     x = torch.empty(0, 64, dtype=BF, device="cuda")
     w = torch.ones(64, dtype=BF, device="cuda")
@@ -155,7 +189,7 @@ def test_gradient_against_differences():
         np.testing.assert_allclose(B.np64(got), num, rtol=1e-4, atol=1e-4)
 
 
-@pytest.mark.parametrize("M,C", [(1, 16), (9, 1152), (300, 2048), (5, 5120), (3, 16384)])
+@pytest.mark.parametrize("M,C", [(1, 16), (9, 1152), (300, 2048), (400, 1168), (5, 5120), (3, 16384), (310, 8208)])
 @pytest.mark.parametrize("dtype", [BF, FP16, FP32])
 def test_norm_into_codes(M, C, dtype):
     """Scales within the norm's roundings; a code off by one only where the exact quotient is that near a midpoint."""
@@ -172,8 +206,9 @@ def test_norm_into_codes(M, C, dtype):
     B.within(Q.double(), v / sg, 0.5 + bv / sg + 1e-9, "codes")
 
 
-def test_norm_into_codes_matches_the_two_calls_in_fp32():
-    x, w, b, _ = case(50, 768, FP32, FP32, None)
+@pytest.mark.parametrize("M,C", [(50, 768), (700, 768), (700, 4096)])
+def test_norm_into_codes_matches_the_two_calls_in_fp32(M, C):
+    x, w, b, _ = case(M, C, FP32, FP32, None)
     Y, *_ = S.svdq_layernorm(x.cuda(), w.cuda(), b.cuda())
     Q2, s2 = S.svdq_int8_quantize_act(Y)
     Q, s = S.svdq_int8_layernorm_quantize(x.cuda(), w.cuda(), b.cuda())

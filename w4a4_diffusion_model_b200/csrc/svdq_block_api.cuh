@@ -228,30 +228,32 @@ svdq_status launch_int8_single(const svdq::Int8GemmArgs& args, const void* Qx, c
   return SVDQ_OK;
 }
 
-cudaLaunchConfig_t int8_pair_config(int clusters, cudaStream_t st, cudaLaunchAttribute* attr) {
-  cudaLaunchConfig_t cfg = pdl_config(2 * clusters, svdq::kP8Threads, svdq::kP8Bytes, st, attr);
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+// Launch configuration of the pair kernel: clusters of one pair, or two (SPLIT).
+// The attributes are the cluster's size and programmatic stream serialization.
+cudaLaunchConfig_t int8_pair_config(int clusters, int ctas, cudaStream_t st, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = pdl_config(ctas * clusters, svdq::kP8Threads, svdq::kP8Bytes, st, attr + 1);
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cfg;
 }
 
 // Clusters of the pair kernel that fit on the device at once (0: none); also
 // sets the kernel's shared-memory attribute there.
-template <typename OT>
+template <typename OT, bool SPLIT>
 int int8_pair_clusters() {
   static std::atomic<int> cache[kMaxDevices];
   return per_device_once(cache, current_device(), [] {
-    auto kern = svdq::svdq_int8_gemm_pair_kernel<OT>;
+    auto kern = svdq::svdq_int8_gemm_pair_kernel<OT, SPLIT>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, svdq::kP8Bytes) != cudaSuccess) {
       cudaGetLastError();
       return 0;
     }
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = int8_pair_config(sm_count() / 2, nullptr, attr);
-    std::swap(attr[0], attr[1]);
+    cudaLaunchConfig_t cfg = int8_pair_config(1, SPLIT ? 4 : 2, nullptr, attr);
     cfg.numAttrs = 1;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, (void*)kern, &cfg) != cudaSuccess) {
@@ -262,7 +264,7 @@ int int8_pair_clusters() {
   }) - 1;
 }
 
-template <typename OT>
+template <typename OT, bool SPLIT>
 svdq_status launch_int8_pair(const svdq::Int8GemmArgs& a, const void* Qx, const void* Qw, int clusters,
                              cudaStream_t st) {
   CUtensorMap tx, tw, ty;
@@ -281,8 +283,8 @@ svdq_status launch_int8_pair(const svdq::Int8GemmArgs& a, const void* Qx, const 
     return r;
   const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = int8_pair_config((int)std::min<int64_t>(tiles, clusters), st, attr);
-  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::svdq_int8_gemm_pair_kernel<OT>, tx, tw, ty, a, tma_y ? 1 : 0));
+  cudaLaunchConfig_t cfg = int8_pair_config((int)std::min<int64_t>(tiles, clusters), SPLIT ? 4 : 2, st, attr);
+  SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::svdq_int8_gemm_pair_kernel<OT, SPLIT>, tx, tw, ty, a, tma_y ? 1 : 0));
   return SVDQ_OK;
 }
 
@@ -301,16 +303,19 @@ svdq_status launch_int8_few(const svdq::Int8GemmArgs& a, const void* Qx, const v
 
 // Which kernel serves a product, by estimated microseconds on this GPU. The
 // constants are fits to sweeps over M 1..4608, K 1024..13824, N 1024..24576:
-//   0.29 us per 128 bytes of K and wave, whatever the tile (see the kernels);
+//   0.29 us per 128 bytes of K and wave, whatever the tile (see the kernels), or
+//   what L2 delivers: 11.7e6 bytes per us over all CTAs (32 KB each of a pair, 48
+//   KB of a single one);
 //   6.2e6 weight bytes per us where HBM bounds it;
-//   a fixed part of 5.7 for CTA pairs, and for single CTAs 5.1 + 0.033 per row
-//   of the tile with K whole, 5.0 + 0.055 with K halved, 5.7 + 0.046 with K in
-//   quarters (the cluster's sum). Measured, us, pairs against the best single:
-//   16 x 4096 x 4096 15 / 8.8, 64 x 4096 x 24576 29 / 23, 128 x 4096 x 4096
-//   15.4 / 13.8, 128 x 4096 x 12288 17 / 20, 333 x 1360 x 2304 9.7 / 11.5,
-//   1024 x 4096 x 4096 16 / 22.
-// Single CTAs are considered for one wave only: with every SM busy their tiles
-// fetch half as much again per product as a pair's.
+//   a fixed part of 5.7 for CTA pairs, 10.5 with K halved between two pairs, and
+//   for single CTAs 5.1 + 0.033 per row of the tile with K whole, 5.0 + 0.055 with
+//   K halved, 5.7 + 0.046 with K in quarters (the cluster's sum).
+// Measured, us, pairs against the best single: 16 x 4096 x 4096 15 / 8.8,
+// 64 x 4096 x 24576 29 / 23, 128 x 4096 x 4096 15.4 / 13.8, 128 x 4096 x 12288
+// 17 / 20, 333 x 1360 x 2304 9.7 / 11.5, 1024 x 4096 x 4096 16 / 22; pairs whole
+// against halved: 1396 x 10544 x 1088 35.8 / 26.3, 512 x 4096 x 4096 15.5 / 16.3,
+// 1024 x 2048 x 2048 10.6 / 13.5. Single CTAs and halved pairs are considered for
+// one wave only.
 template <typename OT>
 svdq_status launch_int8_linear(const svdq::Int8GemmArgs& a, const void* Qx, const void* Qw, cudaStream_t st) {
   const int64_t weights = (int64_t)a.N * a.K;
@@ -324,25 +329,37 @@ svdq_status launch_int8_linear(const svdq::Int8GemmArgs& a, const void* Qx, cons
     if (a.M <= 4) return launch_int8_few<4, OT>(a, Qx, Qw, st);
     return launch_int8_few<8, OT>(a, Qx, Qw, st);
   }
-  const double k_us = 0.29 * ((a.K + svdq::kI8KTile - 1) / svdq::kI8KTile), hbm_us = (double)weights / 6.2e6;
-  const int clusters = int8_pair_clusters<OT>();
+  const double steps = (a.K + svdq::kI8KTile - 1) / svdq::kI8KTile, hbm_us = (double)weights / 6.2e6;
+  auto step_us = [](double ctas, double bytes) { return std::max(0.29, ctas * bytes / 11.7e6); };
+  const int clusters = int8_pair_clusters<OT, false>();
   const int64_t pairs = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
   const int64_t tiles = (int64_t)((a.M + 127) / 128) * ((a.N + svdq::kI8Cols - 1) / svdq::kI8Cols);
   if (pairs > (1ll << 30)) return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "too many tiles");
-  int best = clusters > 0 ? 0 : 1;               // 0: pairs, else single CTAs with K split that many ways
-  double best_us = clusters > 0 ? 5.7 + std::max(hbm_us, k_us * (double)((pairs + clusters - 1) / clusters)) : 1e30;
+  int best = clusters > 0 ? 0 : 1;   // 0: pairs, -1: pairs with K halved, else single CTAs with K split that many ways
+  double best_us = 1e30;
+  if (clusters > 0)
+    best_us = 5.7 + std::max(hbm_us, steps * step_us(2.0 * (double)std::min<int64_t>(pairs, clusters), svdq::kP8StageBytes) *
+                                         (double)((pairs + clusters - 1) / clusters));
+  if (pairs <= int8_pair_clusters<OT, true>() && steps >= 4) {
+    const double us = 10.5 + std::max(hbm_us, steps / 2 * step_us(4.0 * (double)pairs, svdq::kP8StageBytes));
+    if (us < best_us) {
+      best_us = us;
+      best = -1;
+    }
+  }
   const double rows = (double)std::min(a.M, 128), fixed[3] = {5.1 + 0.033 * rows, 5.0 + 0.055 * rows, 5.7 + 0.046 * rows};
   for (int i = 0; i < 3; ++i) {
     const int splits = 1 << i;
     if (a.K < 2 * splits * svdq::kI8KTile && splits > 1) break;
     if (tiles > int8_single_tiles<OT>(splits)) break;
-    const double us = fixed[i] + std::max(hbm_us, k_us / splits);
+    const double us = fixed[i] + std::max(hbm_us, steps / splits * step_us((double)tiles * splits, svdq::kI8StageBytes));
     if (us < best_us) {
       best_us = us;
       best = splits;
     }
   }
-  if (best == 0) return launch_int8_pair<OT>(a, Qx, Qw, clusters, st);
+  if (best == 0) return launch_int8_pair<OT, false>(a, Qx, Qw, clusters, st);
+  if (best == -1) return launch_int8_pair<OT, true>(a, Qx, Qw, (int)pairs, st);
   if (int8_single_tiles<OT>(best) <= 0) return fail(SVDQ_ERR_CUDA, "svdq_int8_gemm_kernel cannot run on this device");
   return launch_int8_single<OT>(a, Qx, Qw, best, st);
 }

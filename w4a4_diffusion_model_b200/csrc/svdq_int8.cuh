@@ -550,9 +550,92 @@ __device__ __forceinline__ Int8Tile int8_pair_tile(int tile, int tiles_m, int ti
   return Int8Tile{(band * kP8Band + i % rows) * 256, (i / rows) * 256};
 }
 
+// A warp's 32 x 128 band of the int32 tile (tensor memory at taddr, row m0 + lane)
+// to Y: `add` (this lane's 128 int32 in shared memory, or null) is added first;
+// `drained` is told once the last column has left tensor memory.
+template <typename OT, typename F>
+__device__ __forceinline__ void int8_store_band(uint32_t taddr, const int* add, float sx, const float2* colv,
+                                                unsigned char* box, const CUtensorMap& tm_y, int tma_y,
+                                                const Int8GemmArgs& a, int m0, int n0, int lane, F drained) {
+  constexpr int kBoxCols = 128 / (int)sizeof(OT);
+  const bool live = m0 < a.M;
+#pragma unroll
+  for (int b = 0; b < kP8Cols / kBoxCols; ++b) {
+    if (tma_y && lane == 0) bulk_wait_read<0>();   // the previous store from this box has read it
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < kBoxCols; c += 32) {
+      const int col = b * kBoxCols + c;
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(taddr + col, v);
+      tmem_ld_wait();
+      if (col + 32 == kP8Cols) drained();
+      if (add) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const uint4 u = *reinterpret_cast<const uint4*>(add + col + i);
+          v[i] += u.x;
+          v[i + 1] += u.y;
+          v[i + 2] += u.z;
+          v[i + 3] += u.w;
+        }
+      }
+      float f[32];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float4 sb = *reinterpret_cast<const float4*>(colv + col + i);
+        f[i] = fmaf((float)(int)v[i] * sb.x, sx, sb.y);
+        f[i + 1] = fmaf((float)(int)v[i + 1] * sb.z, sx, sb.w);
+      }
+      // row `lane` of the box: 16-byte chunk j at (j ^ (lane & 7)), the 128B swizzle
+      constexpr int kChunks = 32 * (int)sizeof(OT) / 16;
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) {
+        float g[kVecN<OT>];
+#pragma unroll
+        for (int i = 0; i < kVecN<OT>; ++i) g[i] = f[j * kVecN<OT> + i];
+        const int chunk = c * (int)sizeof(OT) / 16 + j;
+        *reinterpret_cast<uint4*>(box + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = pack_vec<OT>(g);
+      }
+    }
+    const int col0 = n0 + b * kBoxCols;
+    if (tma_y) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && live && col0 < a.N) {
+        tma_store_2d_evict_first(&tm_y, box, col0 * (int)sizeof(OT), m0);   // x in bytes
+        bulk_commit();
+      }
+    } else {
+      __syncwarp();
+      const int rows = min(32, a.M - m0);
+      OT* y = static_cast<OT*>(a.y) + (long long)m0 * a.ldy + col0;
+#pragma unroll
+      for (int c = 0; c < kBoxCols; c += 32) {
+        const int e = c + lane, byte = e * (int)sizeof(OT);
+        if (col0 + e < a.N) {
+#pragma unroll 8
+          for (int r = 0; r < rows; ++r)
+            y[r * a.ldy + e] = *reinterpret_cast<const OT*>(box + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
 // tm_y views Y as bytes, in boxes of 32 rows x 128; tma_y = 0 where Y's address or
 // row stride does not allow it (then the staged boxes are written by plain stores).
-template <typename OT>
+//
+// SPLIT: a cluster of two pairs shares one tile, each pair half of K (few tiles and
+// a long K: twice as many SMs work, half as long). Pair p finishes the columns
+// 128 p..; for the other columns each CTA writes its int32 sums into the shared
+// memory of the CTA with the same rows in the other pair (the ring's, idle by
+// then), which adds them to its own.
+constexpr int kP8PartLd = kP8Cols + 4;   // int32 per row of the received half: rows 4 banks apart
+static_assert(kP8Stages * kP8StageBytes >= 128 * kP8PartLd * 4, "the half tile is received in the ring");
+
+template <typename OT, bool SPLIT>
 __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tm_x,
                                                                             const __grid_constant__ CUtensorMap tm_w,
                                                                             const __grid_constant__ CUtensorMap tm_y,
@@ -567,11 +650,15 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
   uint64_t* mma_drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t crank = cluster_ctarank();
-  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  const uint32_t rank = cluster_ctarank(), crank = rank & 1u, even = rank & ~1u;   // CTA of the pair, its even CTA
+  const int part = SPLIT ? (int)(rank >> 1) : 0;
+  constexpr int kCtas = SPLIT ? 4 : 2;
+  const int cluster = blockIdx.x / kCtas, nclusters = gridDim.x / kCtas;
   const int tiles_m = (a.M + 255) / 256, tiles_n = (a.N + 255) / 256;
   const int ntiles = tiles_m * tiles_n;
   const int kts = (a.K + kI8KTile - 1) / kI8KTile;
+  const int kt0 = SPLIT ? kts * part / 2 : 0, kt1 = SPLIT ? kts * (part + 1) / 2 : kts;
+  const uint16_t both = (uint16_t)(3u << even);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kP8Stages; ++s) {
@@ -599,14 +686,31 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
   grid_dependency_wait();
   grid_launch_dependents();
 
+  const int q = warp & 3, h = warp >> 2;      // epilogue warps
+  unsigned char* box = smem + kP8BoxOffset + warp * kP8BoxBytes;
+  float2* colv = reinterpret_cast<float2*>(smem + kP8ColOffset) + warp * kP8Cols;
+  float sx = 0.f;
+  // the scales of a band, ahead of its sums
+  auto load_scales = [&](int m0, int n0) {
+    sx = m0 + lane < a.M ? a.sx[m0 + lane] : 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kP8Cols / 32; ++i) {
+      const int n = n0 + 32 * i + lane;
+      colv[32 * i + lane] = n < a.N ? make_float2(a.sw[n], a.bias ? a.bias[n] : 0.f) : make_float2(0.f, 0.f);
+    }
+    __syncwarp();
+  };
+  bool done = false;                          // SPLIT: this warp's tile is complete
+
   if (warp == 8) {
     if (lane == 0) {
-      const uint32_t full_even = mapa_shared(smem_u32(full), 0);
+      const uint32_t full_even = mapa_shared(smem_u32(full), even);
       uint32_t it = 0;
       bool ok = true;
       for (int tile = cluster; tile < ntiles && ok; tile += nclusters) {
         const Int8Tile t = int8_pair_tile(tile, tiles_m, tiles_n);
-        for (int kt = 0; kt < kts; ++kt, ++it) {
+        for (int kt = kt0; kt < kt1; ++kt, ++it) {
           const uint32_t s = it % kP8Stages;
           if (!mbar_wait(empty + s, ((it / kP8Stages) & 1u) ^ 1u, kDevErrTimeoutEmpty)) {
             ok = false;
@@ -641,7 +745,7 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
           break;
         }
         tc_fence_after();
-        for (int kt = 0; kt < kts; ++kt, ++it) {
+        for (int kt = kt0; kt < kt1; ++kt, ++it) {
           const uint32_t s = it % kP8Stages;
           if (!mbar_wait(full + s, (it / kP8Stages) & 1u, kDevErrTimeoutFull)) {
             ok = false;
@@ -651,99 +755,69 @@ __global__ void __launch_bounds__(kP8Threads, 1) svdq_int8_gemm_pair_kernel(cons
           const uint64_t off = (uint64_t)(s * ((uint32_t)kP8StageBytes >> 4));
 #pragma unroll
           for (int j = 0; j < kI8KTile / 32; ++j)
-            mma_i8_pair(tmem + 256 * buf, dA0 + off + 2u * j, dB0 + off + 2u * j, idesc, (kt | j) != 0 ? 1u : 0u);
-          tc_commit_pair(empty + s, 0x3);
+            mma_i8_pair(tmem + 256 * buf, dA0 + off + 2u * j, dB0 + off + 2u * j, idesc, kt > kt0 || j > 0 ? 1u : 0u);
+          tc_commit_pair(empty + s, both);
         }
-        if (ok) tc_commit_pair(acc_full + buf, 0x3);
+        if (ok) tc_commit_pair(acc_full + buf, both);
       }
       if (!ok) {
-        tc_commit_pair(mma_drain, 0x1);
+        tc_commit_pair(mma_drain, (uint16_t)(1u << even));
         mbar_drain(mma_drain, 0);
       }
     }
+  } else if constexpr (SPLIT) {
+    const Int8Tile t = int8_pair_tile(cluster, tiles_m, tiles_n);
+    if (h == part) load_scales(t.m0 + 128 * (int)crank + 32 * q, t.n0 + 128 * h);
+    done = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0, kDevErrTimeoutAccum) && !device_error_set());
+    tc_fence_after();
   } else {
-    const int q = warp & 3, h = warp >> 2;
-    unsigned char* box = smem + kP8BoxOffset + warp * kP8BoxBytes;
-    float2* colv = reinterpret_cast<float2*>(smem + kP8ColOffset) + warp * kP8Cols;
-    const uint32_t acc_empty_even = mapa_shared(smem_u32(acc_empty), 0);
-    constexpr int kBoxCols = 128 / (int)sizeof(OT);
+    const uint32_t acc_empty_even = mapa_shared(smem_u32(acc_empty), even);
     uint32_t tcount = 0;
     for (int tile = cluster; tile < ntiles; tile += nclusters, ++tcount) {
       const Int8Tile t = int8_pair_tile(tile, tiles_m, tiles_n);
       const uint32_t buf = tcount & 1u;
-      const int m0 = t.m0 + 128 * (int)crank + 32 * q, n0 = t.n0 + kP8Cols * h;
-      const float sx = m0 + lane < a.M ? a.sx[m0 + lane] : 0.f;
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < kP8Cols / 32; ++i) {
-        const int n = n0 + 32 * i + lane;
-        colv[32 * i + lane] = n < a.N ? make_float2(a.sw[n], a.bias ? a.bias[n] : 0.f) : make_float2(0.f, 0.f);
-      }
-      __syncwarp();
-      bool ok = mbar_wait(acc_full + buf, (tcount >> 1) & 1u, kDevErrTimeoutAccum) && !device_error_set();
-      ok = __all_sync(0xFFFFFFFFu, ok);
+      const int m0 = t.m0 + 128 * (int)crank + 32 * q, n0 = t.n0 + 128 * h;
+      load_scales(m0, n0);
+      const bool ok =
+          __all_sync(0xFFFFFFFFu, mbar_wait(acc_full + buf, (tcount >> 1) & 1u, kDevErrTimeoutAccum) && !device_error_set());
       tc_fence_after();
       if (!ok) break;
-      const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + 256 * buf + (uint32_t)(h * kP8Cols);
-      const bool live = m0 < a.M;
-#pragma unroll
-      for (int b = 0; b < kP8Cols / kBoxCols; ++b) {
-        if (tma_y && lane == 0) bulk_wait_read<0>();   // the previous store from this box has read it
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < kBoxCols; c += 32) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(taddr + b * kBoxCols + c, v);
-          tmem_ld_wait();
-          if (b * kBoxCols + c + 32 == kP8Cols) {   // the accumulator is drained
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
-          }
-          float f[32];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float4 sb = *reinterpret_cast<const float4*>(colv + b * kBoxCols + c + i);
-            f[i] = fmaf((float)(int)v[i] * sb.x, sx, sb.y);
-            f[i + 1] = fmaf((float)(int)v[i + 1] * sb.z, sx, sb.w);
-          }
-          // row `lane` of the box: 16-byte chunk j at (j ^ (lane & 7)), the 128B swizzle
-          constexpr int kChunks = 32 * (int)sizeof(OT) / 16;
-#pragma unroll
-          for (int j = 0; j < kChunks; ++j) {
-            float g[kVecN<OT>];
-#pragma unroll
-            for (int i = 0; i < kVecN<OT>; ++i) g[i] = f[j * kVecN<OT> + i];
-            const int chunk = c * (int)sizeof(OT) / 16 + j;
-            *reinterpret_cast<uint4*>(box + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = pack_vec<OT>(g);
-          }
-        }
-        const int col0 = n0 + b * kBoxCols;
-        if (tma_y) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && live && col0 < a.N) {
-            tma_store_2d_evict_first(&tm_y, box, col0 * (int)sizeof(OT), m0);   // x in bytes
-            bulk_commit();
-          }
-        } else {
-          __syncwarp();
-          const int rows = min(32, a.M - m0);
-          OT* y = static_cast<OT*>(a.y) + (long long)m0 * a.ldy + col0;
-#pragma unroll
-          for (int c = 0; c < kBoxCols; c += 32) {
-            const int e = c + lane, byte = e * (int)sizeof(OT);
-            if (col0 + e < a.N) {
-#pragma unroll 8
-              for (int r = 0; r < rows; ++r)
-                y[r * a.ldy + e] = *reinterpret_cast<const OT*>(box + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
-            }
-          }
-          __syncwarp();
-        }
-      }
+      int8_store_band<OT>(tmem + ((uint32_t)(q * 32) << 16) + 256 * buf + (uint32_t)(h * 128), nullptr, sx, colv, box, tm_y,
+                          tma_y, a, m0, n0, lane, [&] {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_remote(acc_empty_even + 8 * buf);
+                          });
     }
     if (lane == 0) bulk_wait<0>();
+  }
+  if constexpr (SPLIT) {
+    __syncwarp();
+    cluster_sync();   // every MMA of the cluster has read its stages: the rings are free
+    const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 128);
+    const uint32_t row = smem_u32(smem) + (uint32_t)((32 * q + lane) * kP8PartLd * 4);
+    if (done && h != part) {
+      const uint32_t there = mapa_shared(row, rank ^ 2u);
+#pragma unroll
+      for (int c = 0; c < kP8Cols; c += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(taddr + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(there + 4 * (c + i)), "r"(v[i]),
+                       "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3])
+                       : "memory");
+      }
+      tc_fence_before();
+    }
+    cluster_sync();   // the halves are there
+    if (done && h == part) {
+      const Int8Tile t = int8_pair_tile(cluster, tiles_m, tiles_n);
+      int8_store_band<OT>(taddr, reinterpret_cast<const int*>(smem) + (32 * q + lane) * kP8PartLd, sx, colv, box, tm_y,
+                          tma_y, a, t.m0 + 128 * (int)crank + 32 * q, t.n0 + 128 * h, lane, [] {});
+      if (lane == 0) bulk_wait<0>();
+    }
   }
   tc_fence_before();
   cluster_sync();   // no CTA leaves while its peer may still signal its barriers
