@@ -19,7 +19,7 @@
 
 #include <cstdint>
 
-#include "svdq_f32x2.cuh"
+#include "svdq_int4.cuh"   // fma2_rn
 
 namespace svdq {
 

@@ -10,7 +10,6 @@
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
-#include "svdq_f32x2.cuh"
 #include "svdq_ptx.cuh"
 
 namespace svdq {
@@ -26,6 +25,18 @@ __host__ __device__ __forceinline__ size_t native_scale_offset(int r, int g, int
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Two IEEE round-to-nearest fp32 products in one instruction.
+__device__ __forceinline__ float2 mul2_rn(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 
 // max(|a|, |b|, |c|).
 __device__ __forceinline__ float max3_abs(float a, float b, float c) {

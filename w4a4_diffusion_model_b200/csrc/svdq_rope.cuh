@@ -20,7 +20,6 @@
 // ahead of the present rows' arithmetic, the first ones ahead of the angles.
 #pragma once
 
-#include "svdq_f32x2.cuh"
 #include "svdq_ptx.cuh"
 #include "svdq_rows.cuh"
 #include "svdq_vec.cuh"

@@ -8,8 +8,9 @@
 // the thread that issues the copies refills the stage behind that barrier.
 #pragma once
 
-#include "svdq_f32x2.cuh"
+#include "svdq_int4.cuh"   // add2_rn, fma2_rn
 #include "svdq_ptx.cuh"
+#include "svdq_quant.cuh"  // mul2_rn
 #include "svdq_vec.cuh"
 
 namespace svdq {
