@@ -139,15 +139,13 @@ svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return with_type(dtype, [&](auto tag) -> svdq_status {
     using T = typename decltype(tag)::type;
-    const int vecs = (int)K / svdq::kVecN<T>;
+    constexpr int NV = 16 / svdq::kVecN<T>;   // 16 values a thread
     const int64_t sms = sm_count();
-    if (vecs <= 128) {   // rows a warp holds: eight of them per block
-      const unsigned grid = (unsigned)std::min<int64_t>((M + 7) / 8, sms * 8);
-      const dim3 block(32, 8);
-      if (vecs <= 32) return launch_int8_quantize<T, 1, 256>(a, grid, block, st);
-      if (vecs <= 64) return launch_int8_quantize<T, 2, 256>(a, grid, block, st);
-      return launch_int8_quantize<T, 4, 256>(a, grid, block, st);
-    }
+    if (K <= 512)   // rows a warp holds: eight of them per block
+      return launch_int8_quantize<T, NV, 256>(a, (unsigned)std::min<int64_t>((M + 7) / 8, sms * 8), dim3(32, 8), st);
+    // Many rows: the ring. Measured, us, ring against one row per block: 9001 x
+    // 13824 68 / 105, 4608 x 4096 12.1 / 19; one row per block has the shorter way
+    // from memory to registers where rows do not queue.
     if (K <= 16384 && M > 2 * sms) {
       using namespace svdq;
       auto go = [&](auto elems, auto warps) -> svdq_status {
@@ -161,9 +159,8 @@ svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_
       return go(Int<32>(), Int<16>());
     }
     const unsigned grid = (unsigned)std::min<int64_t>(M, sms * 8);
-    if (vecs <= 512) return launch_int8_quantize<T, 2, 256>(a, grid, round_up((vecs + 1) / 2, 32), st);
-    if (vecs <= 1024) return launch_int8_quantize<T, 4, 256>(a, grid, round_up((vecs + 3) / 4, 32), st);
-    if (vecs <= 4096) return launch_int8_quantize<T, 4, 1024>(a, grid, round_up((vecs + 3) / 4, 32), st);
+    if (K <= 4096) return launch_int8_quantize<T, NV, 256>(a, grid, round_up((int)(K + 15) / 16, 32), st);
+    if (K <= 16384) return launch_int8_quantize<T, NV, 1024>(a, grid, round_up((int)(K + 15) / 16, 32), st);
     return launch_int8_quantize<T, 0, 1024>(a, grid, 1024, st);
   });
 }
@@ -411,18 +408,17 @@ svdq_status norm_dispatch(const NormCall& n, std::initializer_list<int64_t> stri
   });
 }
 
-// Threads per row and pieces per thread: f gets NV and the block's limit.
-// Pieces: 16-byte vectors, at most 4096 of them, or single values.
-template <bool VEC, typename F>
-svdq_status norm_width(int pieces, F&& f) {
+// Threads per row, and f<pieces per thread, limit of the block's threads>: 16
+// values a thread in 16-byte pieces; single values, 4 or 16 a thread.
+template <typename T, bool VEC, typename F>
+svdq_status norm_width(int C, F&& f) {
   if constexpr (VEC) {
-    if (pieces <= 256) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 512>());
-    if (pieces <= 1024) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 512>());
-    if (pieces <= 2048) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 1024>());
-    return f(std::integral_constant<int, 4>(), std::integral_constant<int, 1024>());
+    constexpr int NV = 16 / svdq::kVecN<T>;
+    const int threads = round_up((C + 15) / 16, 32);
+    return threads <= 256 ? f(threads, Int<NV>(), Int<256>()) : f(threads, Int<NV>(), Int<1024>());
   } else {
-    if (pieces <= 2048) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 512>());
-    return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1024>());
+    if (C <= 2048) return f(round_up((C + 3) / 4, 32), Int<4>(), Int<512>());
+    return f(round_up((C + 15) / 16, 32), Int<16>(), Int<1024>());
   }
 }
 
@@ -432,8 +428,8 @@ svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStr
     using T = typename decltype(tag)::type;
     using WT = typename decltype(wtag)::type;
     constexpr bool VEC = decltype(vec)::value;
-    const int pieces = (int)n.C / (VEC ? svdq::kVecN<T> : 1);
     if constexpr (VEC) {
+      // many rows: the ring (9216 x 4096 26 us, one row per block 54)
       if (n.C > 512 && n.M > 2 * sm_count()) {
         using namespace svdq;
         const size_t row = (size_t)n.C * sizeof(T);
@@ -448,9 +444,8 @@ svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStr
         return go(Int<32>(), Int<16>());
       }
     }
-    return norm_width<VEC>(pieces, [&](auto nv, auto maxt) -> svdq_status {
+    return norm_width<T, VEC>((int)n.C, [&](int threads, auto nv, auto maxt) -> svdq_status {
       constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
-      const int threads = round_up((pieces + NV - 1) / NV, 32);
       const dim3 block(threads, threads == 32 ? 8 : 1);
       const unsigned grid = (unsigned)std::min<int64_t>((n.M + block.y - 1) / block.y, (int64_t)sm_count() * 16);
       cudaLaunchAttribute attr[1];
@@ -672,7 +667,6 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
     using T = typename decltype(tag)::type;
     using WT = typename decltype(wtag)::type;
     constexpr bool VEC = decltype(vec)::value;
-    const int pieces = (int)n.C / (VEC ? svdq::kVecN<T> : 1);
     if constexpr (VEC) {
       if (n.C > 512) {
         using namespace svdq;
@@ -700,17 +694,19 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
         return size(Int<32>(), Int<16>(), Int<1>(), std::false_type());
       }
     }
-    return norm_width<VEC>(pieces, [&](auto nv, auto maxt) -> svdq_status {
+    // rows of a warp, or single values
+    auto teams = [&](int threads, auto nv, auto maxt) -> svdq_status {
       constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
       constexpr int N = VEC ? svdq::kVecN<T> : 1;
-      const int threads = round_up((pieces + NV - 1) / NV, 32);
-      const dim3 block(threads, std::max(1, std::min(512 / threads, 8)));
+      const dim3 block(threads, std::max(1, std::min(std::min(MAXT, 512) / threads, 8)));
       const size_t smem = block.y > 1 ? (size_t)NV * N * threads * 4 : 0;
       cudaLaunchAttribute attr[1];
       cudaLaunchConfig_t cfg = pdl_config((unsigned)(groups * a.chunks), block, smem, st, attr);
       SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::layernorm_backward_kernel<T, WT, NV, MAXT, VEC>, a));
       return SVDQ_OK;
-    });
+    };
+    if constexpr (VEC) return teams(32, Int<16 / svdq::kVecN<T>>(), Int<256>());
+    else return norm_width<T, VEC>((int)n.C, teams);
   });
   if (r != SVDQ_OK || !a.part) return r;
   const int64_t cols = groups * C;
