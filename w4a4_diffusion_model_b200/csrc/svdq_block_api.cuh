@@ -60,6 +60,13 @@ svdq_status with_type(int dtype, F&& f) {
 
 int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
+// Lanes that hold a row of up to 512 values, 16 each: a power of two.
+int team_lanes(int values) {
+  int lanes = 1;
+  while (lanes < 32 && lanes * 16 < values) lanes *= 2;
+  return lanes;
+}
+
 // Kernels that stream rows through a ring (svdq_rows.cuh) run 512 threads per SM
 // (640 in the backward pass up to 320 a block); the blocks share 192 KB, less
 // `other` bytes each, for their stages: at least one and at most kRingMaxStages.
@@ -141,8 +148,11 @@ svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_
     using T = typename decltype(tag)::type;
     constexpr int NV = 16 / svdq::kVecN<T>;   // 16 values a thread
     const int64_t sms = sm_count();
-    if (K <= 512)   // rows a warp holds: eight of them per block
-      return launch_int8_quantize<T, NV, 256>(a, (unsigned)std::min<int64_t>((M + 7) / 8, sms * 8), dim3(32, 8), st);
+    if (K <= 512) {   // rows that a warp, or some of its lanes, hold
+      const int lanes = team_lanes((int)K), teams = 256 / lanes;
+      return launch_int8_quantize<T, NV, 256>(a, (unsigned)std::min<int64_t>((M + teams - 1) / teams, sms * 8),
+                                              dim3(lanes, teams), st);
+    }
     // Many rows: the ring. Measured, us, ring against one row per block: 9001 x
     // 13824 68 / 105, 4608 x 4096 12.1 / 19; one row per block has the shorter way
     // from memory to registers where rows do not queue.
@@ -409,12 +419,13 @@ svdq_status norm_dispatch(const NormCall& n, std::initializer_list<int64_t> stri
 }
 
 // Threads per row, and f<pieces per thread, limit of the block's threads>: 16
-// values a thread in 16-byte pieces; single values, 4 or 16 a thread.
+// values a thread in 16-byte pieces (some lanes of a warp up to 512 values); single
+// values, 4 or 16 a thread.
 template <typename T, bool VEC, typename F>
 svdq_status norm_width(int C, F&& f) {
   if constexpr (VEC) {
     constexpr int NV = 16 / svdq::kVecN<T>;
-    const int threads = round_up((C + 15) / 16, 32);
+    const int threads = C <= 512 ? team_lanes(C) : round_up((C + 15) / 16, 32);
     return threads <= 256 ? f(threads, Int<NV>(), Int<256>()) : f(threads, Int<NV>(), Int<1024>());
   } else {
     if (C <= 2048) return f(round_up((C + 3) / 4, 32), Int<4>(), Int<512>());
@@ -446,7 +457,7 @@ svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStr
     }
     return norm_width<T, VEC>((int)n.C, [&](int threads, auto nv, auto maxt) -> svdq_status {
       constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
-      const dim3 block(threads, threads == 32 ? 8 : 1);
+      const dim3 block(threads, threads <= 32 ? 256 / threads : 1);
       const unsigned grid = (unsigned)std::min<int64_t>((n.M + block.y - 1) / block.y, (int64_t)sm_count() * 16);
       cudaLaunchAttribute attr[1];
       cudaLaunchConfig_t cfg = pdl_config(grid, block, 0, st, attr);
@@ -694,18 +705,18 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
         return size(Int<32>(), Int<16>(), Int<1>(), std::false_type());
       }
     }
-    // rows of a warp, or single values
+    // rows of lanes of a warp, or single values
     auto teams = [&](int threads, auto nv, auto maxt) -> svdq_status {
       constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
-      constexpr int N = VEC ? svdq::kVecN<T> : 1;
-      const dim3 block(threads, std::max(1, std::min(std::min(MAXT, 512) / threads, 8)));
-      const size_t smem = block.y > 1 ? (size_t)NV * N * threads * 4 : 0;
+      const dim3 block(threads, std::max(1, VEC ? MAXT / threads : std::min(512 / threads, 8)));
+      const size_t smem = (size_t)block.y * n.C * 4;   // at most 64 KB
+      ring_blocks_per_sm<svdq::layernorm_backward_kernel<T, WT, NV, MAXT, VEC>>(threads, smem);   // sets the attribute
       cudaLaunchAttribute attr[1];
       cudaLaunchConfig_t cfg = pdl_config((unsigned)(groups * a.chunks), block, smem, st, attr);
       SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::layernorm_backward_kernel<T, WT, NV, MAXT, VEC>, a));
       return SVDQ_OK;
     };
-    if constexpr (VEC) return teams(32, Int<16 / svdq::kVecN<T>>(), Int<256>());
+    if constexpr (VEC) return teams(team_lanes((int)n.C), Int<16 / svdq::kVecN<T>>(), Int<256>());
     else return norm_width<T, VEC>((int)n.C, teams);
   });
   if (r != SVDQ_OK || !a.part) return r;

@@ -39,8 +39,8 @@ __device__ __forceinline__ void int8_values(const Int8QuantArgs& a, const uint4&
   }
 }
 
-// A team of blockDim.x threads (a warp, or the whole block) takes a row at a
-// time and holds it in registers, NV vectors a thread: one read of X, one
+// A team of blockDim.x threads (lanes of a warp, or the whole block) takes a row
+// at a time and holds it in registers, NV vectors a thread: one read of X, one
 // write of the codes, which is the bound (HBM). NV = 0: the row does not fit;
 // it is read once for its maximum and once more, from L2, for its codes.
 template <typename T, int NV, int MAXT>
@@ -48,13 +48,16 @@ __global__ void __launch_bounds__(MAXT, 1) int8_quantize_kernel(const Int8QuantA
   constexpr int N = kVecN<T>;
   constexpr int R = NV ? NV : 1;
   __shared__ float2 slots[2][32];
-  const int warps = blockDim.x >> 5, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   const int step = (int)blockDim.x * N;
   grid_dependency_wait();
   grid_launch_dependents();
   const long long teams = (long long)gridDim.x * blockDim.y;
   int turn = 0;
-  for (long long m = (long long)blockIdx.x * blockDim.y + threadIdx.y; m < a.M; m += teams, turn ^= 1) {
+  // the lanes of a warp make the same number of turns, rows or not
+  for (long long first = (long long)blockIdx.x * blockDim.y; first < a.M; first += teams, turn ^= 1) {
+    const long long m = first + threadIdx.y;
+    const int K = m < a.M ? a.K : 0;
     const T* x = static_cast<const T*>(a.x) + m * a.ldx;
     uint4 r[R];
     float amax = 0.f;
@@ -68,31 +71,31 @@ __global__ void __launch_bounds__(MAXT, 1) int8_quantize_kernel(const Int8QuantA
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int k = v * step + tid * N;
-        r[v] = k < a.K ? load_once(x + k) : make_uint4(0, 0, 0, 0);
+        r[v] = k < K ? load_once(x + k) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int k = v * step + tid * N;
-        if (k < a.K) look(r[v], k);
+        if (k < K) look(r[v], k);
       }
     } else {
-      for (int k = tid * N; k < a.K; k += step) look(*reinterpret_cast<const uint4*>(x + k), k);
+      for (int k = tid * N; k < K; k += step) look(*reinterpret_cast<const uint4*>(x + k), k);
     }
-    const Int8Scale sc = int8_scale(team_max_nan(amax, warps, slots[turn]));
-    if (tid == 0) a.s[m] = sc.s;
+    const Int8Scale sc = int8_scale(team_max_nan(amax, slots[turn]));
+    if (tid == 0 && K > 0) a.s[m] = sc.s;
     int8_t* q = a.q + m * a.K;
     if constexpr (NV > 0) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int k = v * step + tid * N;
-        if (k < a.K) {
+        if (k < K) {
           float f[N];
           int8_values<T>(a, r[v], k, f);
           int8_store<N>(q + k, f, sc);
         }
       }
     } else {
-      for (int k = tid * N; k < a.K; k += step) {
+      for (int k = tid * N; k < K; k += step) {
         float f[N];
         int8_values<T>(a, *reinterpret_cast<const uint4*>(x + k), k, f);
         int8_store<N>(q + k, f, sc);

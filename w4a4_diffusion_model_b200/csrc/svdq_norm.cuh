@@ -65,28 +65,31 @@ __device__ __forceinline__ void norm_gain(const NormArgs& a, long long g, int c,
   }
 }
 
-// A team of blockDim.x threads takes a row at a time: a warp (several teams
-// in the block: blockDim.y) or the whole block (blockDim.y == 1). A thread
+// A team of blockDim.x threads takes a row at a time: some lanes of a warp or a
+// warp (several teams in the block: blockDim.y) or the whole block. A thread
 // holds NV pieces of the row.
 template <typename T, typename WT, int NV, int MAXT, bool VEC, bool QUANT>
 __global__ void __launch_bounds__(MAXT, 1) layernorm_kernel(const NormArgs a) {
   using P = Piece<T, VEC>;
   constexpr int N = P::kN;
   __shared__ float2 slots[3][32];
-  const int warps = blockDim.x >> 5, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   const float inv_c = 1.f / (float)a.C;
   grid_dependency_wait();
   grid_launch_dependents();
   const long long teams = (long long)gridDim.x * blockDim.y;
-  for (long long m = (long long)blockIdx.x * blockDim.y + threadIdx.y; m < a.M; m += teams) {
+  // the lanes of a warp make the same number of turns, rows or not
+  for (long long first = (long long)blockIdx.x * blockDim.y; first < a.M; first += teams) {
+    const long long m = first + threadIdx.y;
+    const bool live = m < a.M;
     const T* x = static_cast<const T*>(a.x) + m * a.ldx;
     typename P::Raw r[NV];
+    float sum = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * (int)blockDim.x + tid) * N;
-      r[v] = c < a.C ? P::load(x + c) : P::zero();
+      r[v] = live && c < a.C ? P::load(x + c) : P::zero();
     }
-    float sum = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float f[N];
@@ -94,7 +97,7 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_kernel(const NormArgs a) {
 #pragma unroll
       for (int i = 0; i < N; ++i) sum += f[i];
     }
-    const float mean = team_sum(sum, warps, slots[0]) * inv_c;
+    const float mean = team_sum(sum, slots[0]) * inv_c;
     float sq = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -105,12 +108,12 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_kernel(const NormArgs a) {
         for (int i = 0; i < N; ++i) sq = fmaf(f[i] - mean, f[i] - mean, sq);
       }
     }
-    const float rstd = __frsqrt_rn(fmaf(team_sum(sq, warps, slots[1]), inv_c, a.eps));
-    if (tid == 0) {
+    const float rstd = __frsqrt_rn(fmaf(team_sum(sq, slots[1]), inv_c, a.eps));
+    if (live && tid == 0) {
       if (a.mean) a.mean[m] = mean;
       if (a.rstd) a.rstd[m] = rstd;
     }
-    const long long g = m / a.rows_per_group;
+    const long long g = (unsigned)(live ? m : first) / (unsigned)a.rows_per_group;
     auto value = [&](int v, int c, float (&f)[N]) {
       float w[N], b[N];
       P::unpack(r[v], f);
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_kernel(const NormArgs a) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int c = (v * (int)blockDim.x + tid) * N;
-        if (c < a.C) {
+        if (live && c < a.C) {
           float f[N];
           value(v, c, f);
           P::store(static_cast<T*>(a.y) + m * a.ldy + c, f);
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_kernel(const NormArgs a) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int c = (v * (int)blockDim.x + tid) * N;
-        if (c < a.C) {
+        if (live && c < a.C) {
           value(v, c, q[v]);
           if (a.inv_lambda) {
             float l[N];
@@ -146,12 +149,12 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_kernel(const NormArgs a) {
           for (int i = 0; i < N; ++i) amax = max_nan(amax, fabsf(q[v][i]));
         }
       }
-      const Int8Scale sc = int8_scale(team_max_nan(amax, warps, slots[2]));
-      if (tid == 0) a.s[m] = sc.s;
+      const Int8Scale sc = int8_scale(team_max_nan(amax, slots[2]));
+      if (live && tid == 0) a.s[m] = sc.s;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int c = (v * (int)blockDim.x + tid) * N;
-        if (c < a.C) int8_store<N>(a.q + m * a.C + c, q[v], sc);
+        if (live && c < a.C) int8_store<N>(a.q + m * a.C + c, q[v], sc);
       }
     }
   }
@@ -334,7 +337,7 @@ template <typename T, typename WT, int NV, int MAXT, bool VEC>
 __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormArgs a) {
   using P = Piece<T, VEC>;
   constexpr int N = P::kN;
-  extern __shared__ float norm_smem[];      // [NV * N][blockDim.x]: the teams' sums, one team at a time
+  extern __shared__ float norm_smem[];      // [teams][C]: the teams' sums
   __shared__ float2 slots[2][32];
   const int tid = threadIdx.x, team = threadIdx.y, teams = blockDim.y;
   const int warps = blockDim.x >> 5;
@@ -396,8 +399,8 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormA
       }
     }
     float2 s;
-    if (teams == 1 || warps == 1) {
-      s = team_sum2(s1, s2, warps, slots[turn]);
+    if (teams == 1 || warps <= 1) {
+      s = team_sum2(s1, s2, slots[turn]);
     } else {   // several teams of several warps: every warp leaves its sums, a team adds its own
       s1 = warp_sum(s1);
       s2 = warp_sum(s2);
@@ -423,41 +426,29 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormA
     }
   }
   if (!sums) return;
-  // the teams' sums, in team order, by way of shared memory
-  for (int which = 0; which < 2; ++which) {
-    for (int t = 1; t < teams; ++t) {
-      __syncthreads();
-      if (team == t) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int i = 0; i < N; ++i) norm_smem[(v * N + i) * blockDim.x + tid] = which ? db[v][i] : dw[v][i];
-      }
-      __syncthreads();
-      if (team == 0) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int i = 0; i < N; ++i) (which ? db[v][i] : dw[v][i]) += norm_smem[(v * N + i) * blockDim.x + tid];
-      }
-    }
-  }
-  if (team != 0) return;
+  // the teams' sums, added in team order by way of shared memory
   const long long cols = groups * a.C;
+  const int threads = blockDim.x * blockDim.y, thread = team * blockDim.x + tid;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * (int)blockDim.x + tid) * N;
-    if (c >= a.C) continue;
+  for (int which = 0; which < 2; ++which) {
+    float* out = which ? a.db : a.dw;
+    if (a.part) out = a.part + (2ll * chunk + which) * cols;
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (a.part) {
-        a.part[(2ll * chunk) * cols + g * a.C + c + i] = dw[v][i];
-        a.part[(2ll * chunk + 1) * cols + g * a.C + c + i] = db[v][i];
-      } else {
-        if (a.dw) a.dw[g * a.C + c + i] = dw[v][i];
-        if (a.db) a.db[g * a.C + c + i] = db[v][i];
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * (int)blockDim.x + tid) * N;
+      if (c < a.C) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) norm_smem[team * a.C + c + i] = which ? db[v][i] : dw[v][i];
       }
     }
+    __syncthreads();
+    if (out)
+      for (int c = thread; c < a.C; c += threads) {
+        float t = norm_smem[c];
+        for (int k = 1; k < teams; ++k) t += norm_smem[k * a.C + c];
+        out[g * a.C + c] = t;
+      }
   }
 }
 
@@ -705,7 +696,13 @@ __global__ void __launch_bounds__(kNormFewThreads) layernorm_backward_few_kernel
       s2 = fmaf(h[i], xh[i], s2);
     }
   }
-  const float2 s = team_sum2(s1, s2, team / 32, slot);
+  float2 s = make_float2(warp_sum(s1), warp_sum(s2));
+  if (!narrow) {
+    if (lane == 0) slot[warp] = s;
+    __syncthreads();
+    s = lane < kWarps ? slot[lane] : make_float2(0.f, 0.f);
+    s = make_float2(warp_sum(s.x), warp_sum(s.y));
+  }
   const float m1 = s.x / (float)a.C, m2 = s.y / (float)a.C;
   T* dx = static_cast<T*>(a.dx) + m * a.lddx;
 #pragma unroll 4

@@ -143,35 +143,46 @@ __device__ __forceinline__ float warp_max_nan(float v) {
   return v;
 }
 
-// Sum of two values over the team of `warps` warps that shares a row; every
-// thread gets the result. The team is one warp, or the whole block: then
-// `slot` is 2 x 32 floats of shared memory, and calls that follow each other
-// take alternate slots, so that one barrier per call is enough (a warp can be
-// at most one call behind any other).
-__device__ __forceinline__ float2 team_sum2(float a, float b, int warps, float2* slot) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (warps == 1) return make_float2(a, b);
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Reductions over the team that shares a row; every thread gets the result. The
+// team is the block's blockDim.x threads: a power of two up to a warp (several
+// teams in the block: blockDim.y), or several warps (blockDim.y == 1). Then
+// `slot` is shared memory for a value per warp, and calls that follow each other
+// take alternate slots, so that one barrier per call is enough (a warp can be at
+// most one call behind any other). All lanes of a warp take part, rows or not.
+__device__ __forceinline__ float lanes_sum(float v) {
+  for (int o = min((int)blockDim.x, 32) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float lanes_max_nan(float v) {
+  for (int o = min((int)blockDim.x, 32) >> 1; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+
+__device__ __forceinline__ float2 team_sum2(float a, float b, float2* slot) {
+  a = lanes_sum(a);
+  b = lanes_sum(b);
+  if (blockDim.x <= 32) return make_float2(a, b);
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   if (lane == 0) slot[w] = make_float2(a, b);
   __syncthreads();
   const float2 v = lane < warps ? slot[lane] : make_float2(0.f, 0.f);
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-__device__ __forceinline__ float team_sum(float a, int warps, float2* slot) {
-  a = warp_sum(a);
-  if (warps == 1) return a;
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ float team_sum(float a, float2* slot) {
+  a = lanes_sum(a);
+  if (blockDim.x <= 32) return a;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   if (lane == 0) slot[w].x = a;
   __syncthreads();
   return warp_sum(lane < warps ? slot[lane].x : 0.f);
 }
 
-__device__ __forceinline__ float team_max_nan(float a, int warps, float2* slot) {
-  a = warp_max_nan(a);
-  if (warps == 1) return a;
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ float team_max_nan(float a, float2* slot) {
+  a = lanes_max_nan(a);
+  if (blockDim.x <= 32) return a;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   if (lane == 0) slot[w].x = a;
   __syncthreads();
   return warp_max_nan(lane < warps ? slot[lane].x : 0.f);
