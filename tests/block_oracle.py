@@ -30,11 +30,11 @@ def within(got, want, bound, what=""):
 
 
 def int8_codes(x, mult=None):
-    """(codes, scales) of fp32 values x [M][K]: v = fp32(x mult), s = fp32(max|v| / 127)."""
+    """(codes, scales) of fp32 values x [M][K]: v = fp32(x mult), s = fp32(max|v| fp32(1/127))."""
     v = x.astype(np.float32)
     if mult is not None:
         v = v * mult.astype(np.float32)
-    s = (np.abs(v).max(axis=1) / np.float32(127)).astype(np.float32)
+    s = (np.abs(v).max(axis=1) * (np.float32(1) / np.float32(127))).astype(np.float32)
     safe = np.where(s > 0, s, 1).astype(np.float64)
     q = np.clip(np.rint(v.astype(np.float64) / safe[:, None]), -127, 127)
     return np.where(s[:, None] > 0, q, 0).astype(np.int64), s

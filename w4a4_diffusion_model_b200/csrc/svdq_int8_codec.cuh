@@ -1,5 +1,5 @@
 // The 8-bit integer codec: one fp32 scale per row,
-//   s = fp32(max|v| / 127),   q = clamp(RNE(v / s), -127, 127)
+//   s = fp32(max|v| * fp32(1/127)),   q = clamp(RNE(v / s), -127, 127)
 // of the exact real quotient (ties to even); s == 0 gives codes 0; a row that
 // holds an infinity or a NaN gets the scale NaN and codes 0, so that what is
 // computed from it is NaN.
@@ -32,7 +32,7 @@ struct Int8Scale {
 __device__ __forceinline__ Int8Scale int8_scale(float amax) {
   if (!(amax <= 3.4028235e38f)) return Int8Scale{__int_as_float(0x7FC00000), 0.f, true};
   Int8Scale r;
-  r.s = __fdiv_rn(amax, 127.f);
+  r.s = amax * (1.f / 127.f);
   r.special = r.s < 1e-30f && r.s > 0.f;
   r.rcp = r.s >= 1e-30f ? __frcp_rn(r.s) : 0.f;
   return r;

@@ -512,30 +512,28 @@ def _norm_params(X: torch.Tensor, weight: torch.Tensor | None, bias: torch.Tenso
     M, C = X.shape
     first = weight if weight is not None else bias
     if first is None:
-        if rows_per_group and rows_per_group < 0:
-            raise ValueError("rows_per_group must not be negative")
         rows = rows_per_group or 0
-        groups = max(1, -(-M // rows)) if rows else 1
-        return DTYPES[X.dtype], None, None, rows, groups
-    if first.dtype != X.dtype and first.dtype != torch.float32:
+        if rows < 0:
+            raise ValueError("rows_per_group must not be negative")
+        return _FLOAT_TYPES[X.dtype], None, None, rows, -(-M // rows) if rows and M else 1
+    dtype, shape = first.dtype, first.shape
+    if dtype is not X.dtype and dtype is not torch.float32:
         raise ValueError(f"weight and bias must be {X.dtype} or torch.float32")
-    if first.dim() == 1:
+    if len(shape) == 1:
         if rows_per_group:
             raise ValueError("weight and bias of row groups are [groups][C]")
-        shape, rows, groups = (C,), 0, 1
+        rows, groups, want = 0, 1, (C,)
     else:
-        groups = first.shape[0]
-        shape = (groups, C)
-        if rows_per_group is None:
+        groups = shape[0]
+        want = (groups, C)
+        rows = rows_per_group
+        if rows is None:
             if groups < 1 or M % groups:
                 raise ValueError(f"{M} rows do not divide into {groups} groups: give rows_per_group")
             rows = M // groups
-        else:
-            rows = rows_per_group
         if M and (rows < 0 or groups != (-(-M // rows) if rows else 1)):
             raise ValueError(f"{M} rows in groups of {rows} do not have {groups} rows of weight and bias")
-    return (DTYPES[first.dtype], _dense(weight, shape, first.dtype, "weight"), _dense(bias, shape, first.dtype, "bias"),
-            rows, groups)
+    return _FLOAT_TYPES[dtype], _dense(weight, want, dtype, "weight"), _dense(bias, want, dtype, "bias"), rows, groups
 
 
 def svdq_layernorm(X: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
