@@ -420,7 +420,7 @@ svdq_status norm_dispatch(const NormCall& n, std::initializer_list<int64_t> stri
 
 // Threads per row, and f<pieces per thread, limit of the block's threads>: 16
 // values a thread in 16-byte pieces (some lanes of a warp up to 512 values); single
-// values, 4 or 16 a thread.
+// values, 4 to 16 a thread.
 template <typename T, bool VEC, typename F>
 svdq_status norm_width(int C, F&& f) {
   if constexpr (VEC) {
@@ -429,6 +429,7 @@ svdq_status norm_width(int C, F&& f) {
     return threads <= 256 ? f(threads, Int<NV>(), Int<256>()) : f(threads, Int<NV>(), Int<1024>());
   } else {
     if (C <= 2048) return f(round_up((C + 3) / 4, 32), Int<4>(), Int<512>());
+    if (C <= 8192) return f(round_up((C + 7) / 8, 32), Int<8>(), Int<1024>());
     return f(round_up((C + 15) / 16, 32), Int<16>(), Int<1024>());
   }
 }
@@ -480,8 +481,11 @@ int64_t norm_chunks(const NormCall& n) {
 // Few rows: one launch that reads them twice instead of two and partial sums.
 // Measured, us, few against ring (bf16): 32 x 1152 2.7 / 5.6, 226 x 1151 4.9 /
 // 9.7, 226 x 4096 6.2 / 8.1, 226 x 8192 9.3 / 11.8 (fp32 13.2 / 12.7), 512 x 2048
-// 6.6 / 6.3, 1024 x 1152 9.6 / 8.2.
-bool norm_few(const NormCall& n) { return n.M <= 256 && n.M * n.C <= (1ll << 21); }
+// 6.6 / 6.3, 1024 x 1152 9.6 / 8.2. Wide rows that no 16-byte pieces fit have no
+// ring to lose to: 400 x 3001 8.0 / 27, 400 x 8763 22 / 54, 1024 x 3001 20 / 35.
+bool norm_few(const NormCall& n) {
+  return (n.M <= 256 && n.M * n.C <= (1ll << 21)) || (n.C % 8 && n.C > 2048 && n.M <= 1024 && n.M * n.C <= (1ll << 23));
+}
 
 size_t norm_workspace_bytes(const NormCall& n) {
   if (norm_few(n)) return 0;
