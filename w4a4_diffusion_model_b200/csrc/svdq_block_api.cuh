@@ -726,7 +726,7 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
   if (r != SVDQ_OK || !a.part) return r;
   const int64_t cols = groups * C;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((cols + 31) / 32), 2), 256, 0, st, attr);
+  cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((cols + 31) / 32), 2), 32 * svdq::kPartWarps, 0, st, attr);
   SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::layernorm_partials_kernel, static_cast<const float*>(a.part), dweight,
                                dbias, (long long)cols, a.chunks));
   return SVDQ_OK;

@@ -150,12 +150,14 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 // take alternate slots, so that one barrier per call is enough (a warp can be at
 // most one call behind any other). All lanes of a warp take part, rows or not.
 __device__ __forceinline__ float lanes_sum(float v) {
-  for (int o = min((int)blockDim.x, 32) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if (blockDim.x >= 32) return warp_sum(v);
+  for (int o = (int)blockDim.x >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
 
 __device__ __forceinline__ float lanes_max_nan(float v) {
-  for (int o = min((int)blockDim.x, 32) >> 1; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  if (blockDim.x >= 32) return warp_max_nan(v);
+  for (int o = (int)blockDim.x >> 1; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
 
