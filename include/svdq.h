@@ -331,7 +331,9 @@ SVDQ_API svdq_status svdq_deltaquant_encode(int64_t F, int64_t H, int64_t W, int
  * 16 bytes, caller-owned memory, asynchronous on `stream`). Each reads its
  * inputs and writes its outputs within the call's work on the stream; calls
  * with buffers of their own may run at once on several streams. An output may
- * be an input's memory only where that is said.
+ * be an input's memory only where that is said, and shares none of its elements
+ * with an input otherwise. A call may be captured into a CUDA graph; the first
+ * one of a kind on a device also sets kernel attributes, so make it before.
  */
 typedef enum { SVDQ_BF16 = 0, SVDQ_FP16 = 1, SVDQ_FP32 = 2, SVDQ_INT32 = 3 } svdq_dtype;
 
@@ -342,7 +344,8 @@ typedef enum { SVDQ_BF16 = 0, SVDQ_FP16 = 1, SVDQ_FP32 = 2, SVDQ_INT32 = 3 } svd
  *   s = fp32(max|v| * fp32(1/127)),  q = clamp(RNE(v / s), -127, 127) of the exact
  *   quotient (ties to even); all 0 if s == 0. A row with an infinity or a NaN
  *   gets the scale NaN and codes 0: what is computed from it is NaN.
- * Writes Qx int8 [M][K] and Sx fp32 [M]. K a multiple of 16, 16 <= K <= 131072.
+ * Writes Qx int8 [M][K] and Sx fp32 [M]. 0 <= M <= 2^30, K a multiple of 16,
+ * 16 <= K <= 131072.
  * (walkthrough eq. (1) with q_max = 127; handbook, Quantization chapter, W8A8.) */
 SVDQ_API svdq_status svdq_int8_quantize_act(int64_t M, int64_t K, int x_dtype, const void* X, int64_t ldx,
                                             const float* inv_lambda, void* Qx, float* Sx, void* stream);
@@ -355,7 +358,7 @@ SVDQ_API svdq_status svdq_int8_quantize_weight(int64_t N, int64_t K, int w_dtype
 /* Y[m][n] = Sx[m] Sw[n] sum_k Qx[m][k] Qw[n][k] + bias[n]: the integer sum is
  * exact; it is rounded to fp32, multiplied by Sw and then Sx, the bias (fp32
  * [N], or NULL) is added with one rounding, and Y (type y_dtype, row stride
- * ldy >= N) takes the result rounded once. Any M >= 0 and N >= 1 (up to 2^24);
+ * ldy >= N) takes the result rounded once. 0 <= M <= 2^30, 1 <= N <= 2^24;
  * codes in [-127, 127] (-128 too); K as above. No workspace. */
 SVDQ_API svdq_status svdq_int8_linear(int64_t M, int64_t K, int64_t N, const void* Qx, const float* Sx,
                                       const void* Qw, const float* Sw, const float* bias, int y_dtype, void* Y,

@@ -49,7 +49,7 @@ def rope(lib, T=4, H=2, D=16, dt=BF, x=GOOD, xt=32, xh=16, y=GOOD, yt=32, yh=16,
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(M=-1), SHAPE), (dict(K=8), SHAPE), (dict(K=24), SHAPE), (dict(K=131088), SHAPE), (dict(M=1 << 31), SHAPE),
+    (dict(M=-1), SHAPE), (dict(K=8), SHAPE), (dict(K=24), SHAPE), (dict(K=131088), SHAPE), (dict(M=(1 << 30) + 1), SHAPE),
     (dict(dt=3), ARG), (dict(dt=-1), ARG), (dict(x=None), ARG), (dict(q=None), ARG), (dict(s=None), ARG),
     (dict(ld=63), ARG), (dict(ld=-64), ARG), (dict(ld=68), ALIGN), (dict(x=BAD), ALIGN), (dict(mult=BAD), ALIGN),
     (dict(q=BAD), ALIGN), (dict(s=BAD), ALIGN)])
@@ -69,7 +69,7 @@ def test_product_refusals(lib, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(M=-1), SHAPE), (dict(C=0), SHAPE), (dict(C=16385, ld=16385, ldy=16385), SHAPE), (dict(dt=3), ARG),
     (dict(wt=FP16), ARG), (dict(rows=-1), ARG), (dict(flags=2), ARG), (dict(eps=-1.0), ARG),
-    (dict(eps=float("nan")), ARG), (dict(x=None), ARG), (dict(y=None), ARG), (dict(ld=63), ARG), (dict(ldy=63), ARG),
+    (dict(eps=float("nan")), ARG), (dict(ldy=72), ARG), (dict(x=None), ARG), (dict(y=None), ARG), (dict(ld=63), ARG), (dict(ldy=63), ARG),
     (dict(x=BAD), ALIGN), (dict(mean=BAD), ALIGN), (dict(rstd=BAD), ALIGN), (dict(w=BAD), ALIGN), (dict(b=BAD), ALIGN)])
 def test_norm_refusals(lib, kw, status):
     assert norm(lib, **kw) == status
@@ -83,7 +83,7 @@ def test_norm_into_codes_refusals(lib):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dy=None), ARG), (dict(mean=None), ARG), (dict(rstd=None), ARG), (dict(dx=None), ARG), (dict(lddy=60), ARG),
-    (dict(lddx=60), ARG), (dict(dx=BAD), ALIGN), (dict(flags=4), ARG), (dict(wt=1), ARG), (dict(C=20000), SHAPE),
+    (dict(lddx=60), ARG), (dict(lddx=72), ARG), (dict(dx=BAD), ALIGN), (dict(flags=4), ARG), (dict(wt=1), ARG), (dict(C=20000), SHAPE),
     (dict(M=5000, dw=GOOD), SMALL), (dict(M=5000, db=GOOD, ws=GOOD, wsb=64), SMALL)])
 def test_backward_refusals(lib, kw, status):
     assert backward(lib, **kw) == status

@@ -36,6 +36,13 @@ svdq_status check_rows(const char* what, int64_t rows, int64_t cols, int64_t ld)
   return SVDQ_OK;
 }
 
+// Two matrices in the same memory have the same row stride.
+svdq_status check_in_place(const char* what, const void* out, int64_t ldo, const void* in, int64_t ldi, int64_t rows) {
+  if (rows > 1 && out == in && ldo != ldi)
+    return fail(SVDQ_ERR_INVALID_ARG, "%s in place: row strides %lld and %lld", what, (long long)ldo, (long long)ldi);
+  return SVDQ_OK;
+}
+
 template <typename T>
 struct Tag {
   using type = T;
@@ -115,7 +122,7 @@ svdq_status launch_rows(Args a, int64_t rows, int64_t cols, int elems, size_t ro
 constexpr int64_t kInt8MaxK = 131072;   // 127^2 K < 2^31
 
 svdq_status check_int8_k(int64_t rows, int64_t K) {
-  if (rows < 0 || rows > (1ll << 31) - 1 || K < 16 || K % 16 || K > kInt8MaxK)
+  if (rows < 0 || rows > (1ll << 30) || K < 16 || K % 16 || K > kInt8MaxK)
     return fail(SVDQ_ERR_UNSUPPORTED_SHAPE, "int8 matrix of %lld x K=%lld: need K a multiple of 16, 16 <= K <= %lld",
                 (long long)rows, (long long)K, (long long)kInt8MaxK);
   return SVDQ_OK;
@@ -582,7 +589,9 @@ svdq_status svdq_layernorm(int64_t M, int64_t C, int dtype, int w_dtype, const v
   if (!(eps >= 0.f)) return fail(SVDQ_ERR_INVALID_ARG, "eps must be >= 0");
   if (M > 0 && (!X || !Y)) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
   if ((r = check_pointers({X, weight, bias, Y, mean, rstd})) != SVDQ_OK) return r;
-  if ((r = check_rows("X", M, C, ldx)) != SVDQ_OK || (r = check_rows("Y", M, C, ldy)) != SVDQ_OK) return r;
+  if ((r = check_rows("X", M, C, ldx)) != SVDQ_OK || (r = check_rows("Y", M, C, ldy)) != SVDQ_OK ||
+      (r = check_in_place("Y", Y, ldy, X, ldx, M)) != SVDQ_OK)
+    return r;
   if ((r = check_device()) != SVDQ_OK) return r;
   if (M == 0) return SVDQ_OK;
   svdq::NormArgs a = {};
@@ -638,7 +647,8 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
   if (M > 0 && (!dY || !X || !mean || !rstd || !dX)) return fail(SVDQ_ERR_INVALID_ARG, "null pointer");
   if ((r = check_pointers({dY, X, weight, mean, rstd, dX, dweight, dbias, workspace})) != SVDQ_OK) return r;
   if ((r = check_rows("dY", M, C, lddy)) != SVDQ_OK || (r = check_rows("X", M, C, ldx)) != SVDQ_OK ||
-      (r = check_rows("dX", M, C, lddx)) != SVDQ_OK)
+      (r = check_rows("dX", M, C, lddx)) != SVDQ_OK || (r = check_in_place("dX", dX, lddx, dY, lddy, M)) != SVDQ_OK ||
+      (r = check_in_place("dX", dX, lddx, X, ldx, M)) != SVDQ_OK)
     return r;
   const bool sums = dweight || dbias;
   const size_t need = sums ? norm_workspace_bytes(n) : 0;

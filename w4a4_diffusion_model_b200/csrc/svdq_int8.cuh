@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) int8_quantize_rows_kernel(cons
       if (in[v]) int8_store<N>(q + v * (int)blockDim.x * N, f[v], sc);
     q += q_step;
   }
+  if (tid == 0) ring.leave();
 }
 
 // ---------------------------------------------------------------- tensor-core pieces

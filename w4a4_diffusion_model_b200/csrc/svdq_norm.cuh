@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) layernorm_rows_kernel(const No
         if (in[v]) int8_store<N>(a.q + (long long)m * a.C + (v * (int)blockDim.x + tid) * N, f[v], sc);
     }
   }
+  if (tid == 0) ring.leave();
 }
 
 // Backward. blockIdx.x = group * chunks + chunk; a block's teams (blockDim.y of
@@ -608,6 +609,7 @@ __global__ void __launch_bounds__(32 * W, BLOCKS) layernorm_backward_rows_kernel
     mean = mean1;
     rstd = rstd1;
   }
+  if (tid == 0) ring.leave();
   if (!a.dw && !a.db) return;
   const long long cols = groups * a.C;
   float* pw = a.part ? a.part + 2ll * chunk * cols : a.dw;

@@ -44,6 +44,14 @@ struct RowRing {
   // the device error; the caller goes on (with what the stage holds), so that
   // the block's barriers stay matched, and every later wait returns at once.
   __device__ void wait(int stage, uint32_t parity) { mbar_wait(full + stage, parity, kDevErrTimeoutFull); }
+  // Thread 0, at the end: after a wait that gave up, a time that no copy in flight
+  // can outlast, before the block's shared memory goes.
+  __device__ void leave() {
+    if (!device_error_set()) return;
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
   __device__ const unsigned char* row(int stage, int mat) const {
     return stages + ((size_t)stage * MATS + mat) * row_bytes;
   }
