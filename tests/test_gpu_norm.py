@@ -123,12 +123,18 @@ def test_many_rows(C):
         run(*case(M, C, dtype, wtype, groups), add_one=groups is not None)
 
 
+@pytest.mark.parametrize("C", [515, 2047, 2051, 2060, 4099, 9001])
+def test_many_rows_of_odd_widths(C):
+    run(*case(320, C, BF, FP32, 2), add_one=True)
+    run(*case(303, C, FP32, FP32, None))
+
+
 def test_many_groups_of_many_rows():
     run(*case(1200, 1024, BF, FP32, 240))
     run(*case(1203, 640, FP16, FP16, 241), rows=5)
 
 
-@pytest.mark.parametrize("M,C", [(40, 96), (700, 96), (200, 1160), (700, 1160), (340, 9000)])
+@pytest.mark.parametrize("M,C", [(40, 96), (700, 96), (200, 1160), (700, 1160), (340, 9000), (300, 2057), (300, 2060)])
 def test_gradient_in_the_memory_of_either_input(M, C):
     x, w, b, dy = (t.cuda() for t in case(M, C, BF, BF, None))
     _, mean, rstd = S.svdq_layernorm(x, w, b)

@@ -485,13 +485,15 @@ int64_t norm_chunks(const NormCall& n) {
   return std::min<int64_t>(per, std::max<int64_t>(1, (norm_group_rows(n) + 3) / 4));
 }
 
-// Few rows: one launch that reads them twice instead of two and partial sums.
+// Few rows, and wide rows that no 16-byte pieces fit (of neither 2 nor 4 byte
+// values): one launch that reads them twice instead of two and partial sums.
 // Measured, us, few against ring (bf16): 32 x 1152 2.7 / 5.6, 226 x 1151 4.9 /
 // 9.7, 226 x 4096 6.2 / 8.1, 226 x 8192 9.3 / 11.8 (fp32 13.2 / 12.7), 512 x 2048
-// 6.6 / 6.3, 1024 x 1152 9.6 / 8.2. Wide rows that no 16-byte pieces fit have no
-// ring to lose to: 400 x 3001 8.0 / 27, 400 x 8763 22 / 54, 1024 x 3001 20 / 35.
+// 6.6 / 6.3, 1024 x 1152 9.6 / 8.2; against single values in registers: 2048 x
+// 3001 38 / 51, 16384 x 3001 275 / 308, 8192 x 8763 333 / 622, 4096 x 1151 68 / 39.
+constexpr int64_t kNormWide = 2048;
 bool norm_few(const NormCall& n) {
-  return (n.M <= 256 && n.M * n.C <= (1ll << 21)) || (n.C % 8 && n.C > 2048 && n.M <= 1024 && n.M * n.C <= (1ll << 23));
+  return (n.M <= 256 && n.M * n.C <= (1ll << 21)) || (n.C > kNormWide && n.C % 4);
 }
 
 size_t norm_workspace_bytes(const NormCall& n) {
@@ -669,29 +671,30 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
   a.chunks = (int)norm_chunks(n);
   a.part = need ? static_cast<float*>(workspace) : nullptr;
   const int64_t groups = norm_groups(n);
-  if (norm_few(n)) {
-    a.strip_blocks = sums ? (int)(groups * ((C + 31) / 32)) : 0;
-    const int rows = (int)(C <= 1024 ? (M + svdq::kNormFewThreads / 32 - 1) / (svdq::kNormFewThreads / 32) : M);
-    // dX in the memory of an input: the sums come first, in a launch of their own
+  // The few-rows form, in one launch; dX in the memory of an input: the sums come
+  // first, in a launch of their own.
+  auto few = [&](auto tag, auto wtag, auto vec) -> svdq_status {
+    auto kern = svdq::layernorm_backward_few_kernel<typename decltype(tag)::type, typename decltype(wtag)::type,
+                                                    decltype(vec)::value>;
     const bool in_place = sums && (overlap(dX, lddx, dY, lddy, n) || overlap(dX, lddx, X, ldx, n));
-    return norm_dispatch(n, {lddy, ldx, lddx}, [&](auto tag, auto wtag, auto vec) -> svdq_status {
-      auto kern = svdq::layernorm_backward_few_kernel<typename decltype(tag)::type, typename decltype(wtag)::type,
-                                                      decltype(vec)::value>;
-      cudaLaunchAttribute attr[1];
-      cudaLaunchConfig_t cfg = pdl_config(in_place ? a.strip_blocks : a.strip_blocks + rows, svdq::kNormFewThreads, 0, st, attr);
+    const int rows = (int)(C <= 1024 ? (M + svdq::kNormFewThreads / 32 - 1) / (svdq::kNormFewThreads / 32) : M);
+    a.strip_blocks = sums ? (int)(groups * ((C + 31) / 32)) : 0;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = pdl_config(in_place ? a.strip_blocks : a.strip_blocks + rows, svdq::kNormFewThreads, 0, st, attr);
+    SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
+    if (in_place) {
+      a.first_block = a.strip_blocks;
+      cfg.gridDim = dim3(rows);
       SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
-      if (in_place) {
-        a.first_block = a.strip_blocks;
-        cfg.gridDim = dim3(rows);
-        SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
-      }
-      return SVDQ_OK;
-    });
-  }
+    }
+    a.part = nullptr;   // nothing to join
+    return SVDQ_OK;
+  };
   r = norm_dispatch(n, {lddy, ldx, lddx}, [&](auto tag, auto wtag, auto vec) -> svdq_status {
     using T = typename decltype(tag)::type;
     using WT = typename decltype(wtag)::type;
     constexpr bool VEC = decltype(vec)::value;
+    if (norm_few(n) || (!VEC && n.C > kNormWide)) return few(tag, wtag, vec);
     if constexpr (VEC) {
       if (n.C > 512) {
         using namespace svdq;
@@ -719,19 +722,15 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
         return size(Int<32>(), Int<16>(), Int<1>(), std::false_type());
       }
     }
-    // rows of lanes of a warp, or single values
-    auto teams = [&](int threads, auto nv, auto maxt) -> svdq_status {
-      constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
-      const dim3 block(threads, std::max(1, VEC ? MAXT / threads : std::min(512 / threads, 8)));
-      const size_t smem = (size_t)block.y * n.C * 4;   // at most 64 KB
-      ring_blocks_per_sm<svdq::layernorm_backward_kernel<T, WT, NV, MAXT, VEC>>(threads, smem);   // sets the attribute
-      cudaLaunchAttribute attr[1];
-      cudaLaunchConfig_t cfg = pdl_config((unsigned)(groups * a.chunks), block, smem, st, attr);
-      SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::layernorm_backward_kernel<T, WT, NV, MAXT, VEC>, a));
-      return SVDQ_OK;
-    };
-    if constexpr (VEC) return teams(team_lanes((int)n.C), Int<16 / svdq::kVecN<T>>(), Int<256>());
-    else return norm_width<T, VEC>((int)n.C, teams);
+    // rows of lanes of a warp, 16 values each in pieces; or 4 single values a thread
+    constexpr int NV = VEC ? 16 / svdq::kVecN<T> : 4, MAXT = VEC ? 256 : 512;
+    const int threads = VEC ? team_lanes((int)n.C) : round_up((int)(n.C + 3) / 4, 32);
+    const dim3 block(threads, std::max(1, VEC ? MAXT / threads : std::min(MAXT / threads, 8)));
+    const size_t smem = (size_t)block.y * n.C * 4;   // at most 16 KB: the teams' values
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = pdl_config((unsigned)(groups * a.chunks), block, smem, st, attr);
+    SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::layernorm_backward_kernel<T, WT, NV, MAXT, VEC>, a));
+    return SVDQ_OK;
   });
   if (r != SVDQ_OK || !a.part) return r;
   const int64_t cols = groups * C;
