@@ -111,10 +111,10 @@ def test_product(M, K, N, dtype):
 
 
 # each kernel and K split, as their sizes choose them: dot products for 1, 2, 4 and 8 tokens; a single CTA's tile with K
-# whole, in halves and in quarters; pairs whole and in halves; each with whole and ragged rows, columns and K
+# whole, in halves, quarters and eighths; pairs whole and in halves; each with whole and ragged rows, columns and K
 @pytest.mark.parametrize("M,K,N", [(1, 1040, 520), (2, 528, 1001), (3, 2064, 300), (7, 4112, 1030),
                                    (16, 4096, 24600), (40, 1360, 24577), (16, 4096, 12288), (13, 4112, 12289),
-                                   (100, 4096, 4096), (77, 4240, 2050), (1024, 1024, 2048), (700, 1104, 4097),
+                                   (100, 4096, 5000), (77, 4240, 5003), (100, 4096, 1024), (33, 4112, 999), (1024, 1024, 2048), (700, 1104, 4097),
                                    (1024, 8192, 1024), (1100, 8208, 1033)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_every_route(M, K, N, dtype):

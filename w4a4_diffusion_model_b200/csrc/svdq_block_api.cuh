@@ -200,8 +200,8 @@ cudaLaunchConfig_t int8_single_config(int64_t tiles, int splits, cudaStream_t st
 // the kernel cannot run); also sets its shared-memory attribute.
 template <typename OT>
 int int8_single_tiles(int splits) {
-  static std::atomic<int> cache[3][kMaxDevices];
-  return per_device_once(cache[splits / 2], current_device(), [splits] {   // splits 1, 2, 4
+  static std::atomic<int> cache[5][kMaxDevices];
+  return per_device_once(cache[splits / 2], current_device(), [splits] {   // splits 1, 2, 4, 8
     auto kern = svdq::svdq_int8_gemm_kernel<OT>;
     int n = 0;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, svdq::kI8Bytes) != cudaSuccess) {
@@ -323,13 +323,16 @@ svdq_status launch_int8_few(const svdq::Int8GemmArgs& a, const void* Qx, const v
 //   6.2e6 weight bytes per us where HBM bounds it;
 //   a fixed part of 5.7 for CTA pairs, 10.5 with K halved between two pairs, and
 //   for single CTAs 5.1 + 0.033 per row of the tile with K whole, 5.0 + 0.055 with
-//   K halved, 5.7 + 0.046 with K in quarters (the cluster's sum).
+//   K halved, 5.7 + 0.046 with K in quarters, 5.0 + 0.047 in eighths (the cluster's
+//   sum).
 // Measured, us, pairs against the best single: 16 x 4096 x 4096 15 / 8.8,
 // 64 x 4096 x 24576 29 / 23, 128 x 4096 x 4096 15.4 / 13.8, 128 x 4096 x 12288
 // 17 / 20, 333 x 1360 x 2304 9.7 / 11.5, 1024 x 4096 x 4096 16 / 22; pairs whole
 // against halved: 1396 x 10544 x 1088 35.8 / 26.3, 512 x 4096 x 4096 15.5 / 16.3,
-// 1024 x 2048 x 2048 10.6 / 13.5. Single CTAs and halved pairs are considered for
-// one wave only.
+// 1024 x 2048 x 2048 10.6 / 13.5; single CTAs in quarters against eighths: 16 x
+// 13824 x 1024 14.3 / 10.5, 178 x 10208 x 380 17.3 / 13.6, 60 x 2048 x 1024 7.7 /
+// 7.0 (16 x 4096 x 4096 8.8 / 14: its 16 clusters of eight do not fit at once).
+// Single CTAs and halved pairs are considered for one wave only.
 template <typename OT>
 svdq_status launch_int8_linear(const svdq::Int8GemmArgs& a, const void* Qx, const void* Qw, cudaStream_t st) {
   const int64_t weights = (int64_t)a.N * a.K;
@@ -361,8 +364,9 @@ svdq_status launch_int8_linear(const svdq::Int8GemmArgs& a, const void* Qx, cons
       best = -1;
     }
   }
-  const double rows = (double)std::min(a.M, 128), fixed[3] = {5.1 + 0.033 * rows, 5.0 + 0.055 * rows, 5.7 + 0.046 * rows};
-  for (int i = 0; i < 3; ++i) {
+  const double rows = (double)std::min(a.M, 128);
+  const double fixed[4] = {5.1 + 0.033 * rows, 5.0 + 0.055 * rows, 5.7 + 0.046 * rows, 5.0 + 0.047 * rows};
+  for (int i = 0; i < 4; ++i) {
     const int splits = 1 << i;
     if (a.K < 2 * splits * svdq::kI8KTile && splits > 1) break;
     if (tiles > int8_single_tiles<OT>(splits)) break;
