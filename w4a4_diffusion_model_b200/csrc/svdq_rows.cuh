@@ -17,8 +17,8 @@ namespace svdq {
 
 constexpr int kRingMaxStages = 8;
 
-// MATS matrices with the same row size; `bytes` of a row is a multiple of 16,
-// and so are the row addresses.
+// MATS matrices with the same row size: row_bytes, the row addresses and the
+// strides are multiples of 16.
 template <int MATS>
 struct RowRing {
   unsigned char* stages;          // [depth][MATS][row_bytes]
@@ -52,9 +52,6 @@ struct RowRing {
     while (globaltimer_ns() - t0 < 1000000ull) {
     }
   }
-  __device__ const unsigned char* row(int stage, int mat) const {
-    return stages + ((size_t)stage * MATS + mat) * row_bytes;
-  }
 };
 
 // A 16-byte piece as pairs of fp32, and back.
@@ -87,7 +84,7 @@ __device__ __forceinline__ void load_pairs(const WT* p, float2 (&f)[N / 2]) {
 
 __device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
 
-// Sums of a and b over a warp in six shuffles: the half-warps take one each.
+// Sums of a and b over a warp in five shuffles: the half-warps take one each.
 // Lanes 0-15 end with the sum of a, lanes 16-31 with the sum of b.
 __device__ __forceinline__ float warp_sum_halves(float a, float b, int lane) {
   const bool hi = (lane & 16) != 0;
@@ -101,7 +98,7 @@ __device__ __forceinline__ float warp_sum_halves(float a, float b, int lane) {
 // The largest |v| of a warp, NaN if any is.
 __device__ __forceinline__ float warp_amax_nan(float v) {
   float r;
-  asm("redux.sync.max.abs.NaN.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+  asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
   return r;
 }
 
