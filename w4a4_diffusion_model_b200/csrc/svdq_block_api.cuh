@@ -493,11 +493,14 @@ int64_t norm_chunks(const NormCall& n) {
 // values): one launch that reads them twice instead of two and partial sums.
 // Measured, us, few against ring (bf16): 32 x 1152 2.7 / 5.6, 226 x 1151 4.9 /
 // 9.7, 226 x 4096 6.2 / 8.1, 226 x 8192 9.3 / 11.8 (fp32 13.2 / 12.7), 512 x 2048
-// 6.6 / 6.3, 1024 x 1152 9.6 / 8.2; against single values in registers: 2048 x
-// 3001 38 / 51, 16384 x 3001 275 / 308, 8192 x 8763 333 / 622, 4096 x 1151 68 / 39.
+// 6.6 / 6.3, 1024 x 1152 9.6 / 8.2; against single values in registers: 400 x 51
+// 6.1 / 5.7, 400 x 691 6.7 / 7.8 (one launch and no workspace are 5 us less on the
+// host), 2048 x 3001 38 / 51, 16384 x 3001 275 / 308, 8192 x 8763 333 / 622,
+// 4096 x 1151 68 / 39.
 constexpr int64_t kNormWide = 2048;
 bool norm_few(const NormCall& n) {
-  return (n.M <= 256 && n.M * n.C <= (1ll << 21)) || (n.C > kNormWide && n.C % 4);
+  const int64_t few = n.M <= 256 ? 1ll << 21 : n.M <= 400 ? 1ll << 20 : 0;
+  return n.M * n.C <= few || (n.C > kNormWide && n.C % 4);
 }
 
 size_t norm_workspace_bytes(const NormCall& n) {
