@@ -235,3 +235,60 @@ def test_captured_backward():
     _, m2, r2 = S.svdq_layernorm(x, w, b)
     for a, c in zip(out, S.svdq_layernorm_backward(dy, x, w, m2, r2)):
         assert torch.equal(a, c)
+
+
+# off 16-byte boundaries, many rows: one warp a row (4 and 8 values a thread), several rows of several warps in a
+# block, one row, sixteen warps; rows that leave teams and chunks idle
+@pytest.mark.parametrize("M,C", [(701, 1), (1203, 51), (997, 127), (1501, 129), (1400, 251), (650, 571), (1100, 1151),
+                                 (420, 2044), (403, 2049), (450, 4090), (405, 4095)])
+@pytest.mark.parametrize("dtype,wtype", [(BF, BF), (FP16, FP32), (FP32, FP32)])
+def test_single_values(M, C, dtype, wtype):
+    if C % (4 if dtype == FP32 else 8) == 0:
+        pytest.skip("fits 16-byte pieces")
+    run(*case(M, C, dtype, wtype, None, 1))
+
+
+@pytest.mark.parametrize("M,C,groups,rows", [(903, 51, 3, None), (1404, 381, 4, None), (1000, 381, 3, 401),
+                                             (405, 571, 405, None), (502, 1151, 2, None), (460, 2501, 230, None)])
+@pytest.mark.parametrize("add_one", [False, True])
+def test_single_values_in_groups(M, C, groups, rows, add_one):
+    run(*case(M, C, BF, FP32, groups, 2), rows=rows, add_one=add_one)
+
+
+@pytest.mark.parametrize("M,C,pad", [(900, 120, 3), (700, 571, 0), (500, 3000, 1)])
+def test_single_values_in_place(M, C, pad):
+    """Strides off 16-byte boundaries; the next row is loaded before this one's result is stored over it."""
+    x, w, b, dy = case(M, C, BF, BF, None, 3)
+    _, mean, rstd, *_ = run(x, w, b, dy)
+    X, dY = (torch.empty(M, C + pad, dtype=BF, device="cuda")[:, :C].copy_(t) for t in (x, dy))
+    W = w.cuda()
+    got, gw, gb = S.svdq_layernorm_backward(dY, X, W, mean, rstd)
+    over, ow, ob = S.svdq_layernorm_backward(dY, X, W, mean, rstd, out=dY)
+    assert over.data_ptr() == dY.data_ptr() and torch.equal(over, got) and torch.equal(ow, gw) and torch.equal(ob, gb)
+    out, m2, r2 = S.svdq_layernorm(X, W, b.cuda())
+    same, m3, r3 = S.svdq_layernorm(X, W, b.cuda(), out=X)
+    assert same.data_ptr() == X.data_ptr() and torch.equal(same, out) and torch.equal(m2, m3) and torch.equal(r2, r3)
+
+
+@pytest.mark.parametrize("C", [51, 381, 1151, 2501])
+def test_single_values_with_large_means(C):
+    """The variance of values far from zero, and of a column range that differs from the rest."""
+    x, w, b, dy = case(450, C, FP32, FP32, None, 4)
+    x[::2] += 1000.0
+    x[1::2, : C // 3] += 500.0
+    run(x, w, b, dy)
+
+
+@pytest.mark.parametrize("C", [381, 1151, 2501])
+def test_single_values_nan_and_infinity_stay_in_their_rows(C):
+    x, w, b, dy = (t.cuda() for t in case(600, C, BF, BF, None, 5))
+    Y, mean, rstd = S.svdq_layernorm(x, w, b)
+    dX, *_ = S.svdq_layernorm_backward(dy, x, w, mean, rstd)
+    z = x.clone()
+    z[7, 3], z[500, C - 1] = float("nan"), float("inf")
+    Y2, mean2, rstd2 = S.svdq_layernorm(z, w, b)
+    dX2, *_ = S.svdq_layernorm_backward(dy, z, w, mean2, rstd2)
+    keep = torch.ones(600, dtype=torch.bool, device="cuda")
+    keep[[7, 500]] = False
+    assert torch.equal(Y[keep], Y2[keep]) and torch.equal(dX[keep], dX2[keep])
+    assert Y2[~keep].isnan().all() and dX2[~keep].isnan().all()

@@ -431,7 +431,7 @@ svdq_status norm_dispatch(const NormCall& n, std::initializer_list<int64_t> stri
 
 // Threads per row, and f<pieces per thread, limit of the block's threads>: 16
 // values a thread in 16-byte pieces (some lanes of a warp up to 512 values); single
-// values, 4 to 16 a thread.
+// values, 4 to 16 a thread (up to kNormValues only for the form that ends in codes).
 template <typename T, bool VEC, typename F>
 svdq_status norm_width(int C, F&& f) {
   if constexpr (VEC) {
@@ -445,8 +445,20 @@ svdq_status norm_width(int C, F&& f) {
   }
 }
 
+// Rows of single values up to kNormValues: threads of a row, 4 or 8 values each,
+// threads of a block (whole rows side by side), and f<values a thread, threads>.
+constexpr int64_t kNormValues = 4096;
+int value_lanes(int64_t C) { return C <= 128 ? 32 : round_up((int)(C + 7) / 8, 32); }
+int value_limit(int64_t C) { return C <= 2048 ? 256 : 512; }
+template <typename F>
+svdq_status value_width(int64_t C, F&& f) {
+  if (C <= 128) return f(Int<4>(), Int<256>());
+  if (C <= 2048) return f(Int<8>(), Int<256>());
+  return f(Int<8>(), Int<512>());
+}
+
 template <bool QUANT>
-svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStream_t st) {
+svdq_status launch_layernorm(const NormCall& n, svdq::NormArgs a, cudaStream_t st) {
   return norm_dispatch(n, {a.ldx, QUANT ? (int64_t)0 : (int64_t)a.ldy}, [&](auto tag, auto wtag, auto vec) -> svdq_status {
     using T = typename decltype(tag)::type;
     using WT = typename decltype(wtag)::type;
@@ -467,6 +479,20 @@ svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStr
         return go(Int<32>(), Int<16>());
       }
     }
+    if constexpr (!VEC && !QUANT) {
+      if (n.C <= kNormValues)
+        return value_width(n.C, [&](auto nv, auto maxt) -> svdq_status {
+          constexpr int MAXT = decltype(maxt)::value;
+          const int64_t groups = norm_groups(n), rows = norm_group_rows(n);
+          const int lanes = value_lanes(n.C), teams = (int)std::min<int64_t>(MAXT / lanes, rows);
+          const int64_t per_sm = (MAXT > 256 ? MAXT : 3 * MAXT) / (lanes * teams);   // as many as are resident
+          a.chunks = (int)std::min<int64_t>(std::max<int64_t>(1, per_sm * sm_count() / groups), (rows + teams - 1) / teams);
+          cudaLaunchAttribute attr[1];
+          cudaLaunchConfig_t cfg = pdl_config((unsigned)(groups * a.chunks), dim3(lanes, teams), 0, st, attr);
+          SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::layernorm_values_kernel<T, WT, decltype(nv)::value, MAXT>, a));
+          return SVDQ_OK;
+        });
+    }
     return norm_width<T, VEC>((int)n.C, [&](int threads, auto nv, auto maxt) -> svdq_status {
       constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
       const dim3 block(threads, threads <= 32 ? 256 / threads : 1);
@@ -479,28 +505,35 @@ svdq_status launch_layernorm(const NormCall& n, const svdq::NormArgs& a, cudaStr
   });
 }
 
-// Row chunks per group of the backward pass: blocks of about 640 threads in all
-// per SM (16 channels a thread), over all groups. More groups than that: each
-// block takes a group's rows alone, and no partial sums are kept.
+// Row chunks per group of the backward pass, over all groups as many blocks per SM
+// as are resident at once or, in the ring, blocks of about 640 threads in all (16
+// channels a thread). More groups than that: each block takes a group's rows
+// alone, and no partial sums are kept. (Single values: 4 blocks per SM 4133 x 338
+// 14.9 against 11.8 us, 14324 x 571 36.0 against 34.6.)
 int64_t norm_chunks(const NormCall& n) {
   const int64_t groups = norm_groups(n);
-  const int64_t per_sm = n.C <= 512 ? 2 : std::max<int64_t>(1, 640 / round_up((int)(n.C + 15) / 16, 32));
+  int64_t per_sm = 2;
+  if (n.C % (n.dtype == SVDQ_FP32 ? 4 : 8)) {
+    const int lanes = value_lanes(n.C), limit = value_limit(n.C);
+    if (n.C <= kNormValues) per_sm = 512 / (limit / lanes * lanes);
+  } else if (n.C > 512) {
+    per_sm = std::max<int64_t>(1, 640 / round_up((int)(n.C + 15) / 16, 32));
+  }
   const int64_t per = std::max<int64_t>(1, per_sm * sm_count() / groups);
   return std::min<int64_t>(per, std::max<int64_t>(1, (norm_group_rows(n) + 3) / 4));
 }
 
-// Few rows, and wide rows that no 16-byte pieces fit (of neither 2 nor 4 byte
-// values): one launch that reads them twice instead of two and partial sums.
-// Measured, us, few against ring (bf16): 32 x 1152 2.7 / 5.6, 226 x 1151 4.9 /
-// 9.7, 226 x 4096 6.2 / 8.1, 226 x 8192 9.3 / 11.8 (fp32 13.2 / 12.7), 512 x 2048
-// 6.6 / 6.3, 1024 x 1152 9.6 / 8.2; against single values in registers: 400 x 51
-// 6.1 / 5.7, 400 x 691 6.7 / 7.8 (one launch and no workspace are 5 us less on the
-// host), 2048 x 3001 38 / 51, 16384 x 3001 275 / 308, 8192 x 8763 333 / 622,
-// 4096 x 1151 68 / 39.
-constexpr int64_t kNormWide = 2048;
+// Few rows, and rows too wide for single values in registers: one launch that reads
+// them twice instead of two and partial sums. Measured, us, few against ring
+// (bf16): 32 x 1152 2.7 / 5.6, 226 x 4096 6.2 / 8.1, 226 x 8192 9.3 / 11.8 (fp32
+// 13.2 / 12.7), 512 x 2048 6.6 / 6.3, 1024 x 1152 9.6 / 8.2; against single values:
+// 32 x 1151 3.4 / 7.4, 226 x 1151 fp32 4.7 / 7.7, 400 x 691 6.8 / 7.8, 400 x 51 6.2 /
+// 5.2 (one launch and no workspace are 5 us less on the host), 2048 x 3001 38 / 23,
+// 4096 x 1151 68 / 18; 16 values a thread, of 1024, without the next row's loads:
+// 8192 x 8763 333 / 622.
 bool norm_few(const NormCall& n) {
   const int64_t few = n.M <= 256 ? 1ll << 21 : n.M <= 400 ? 1ll << 20 : 0;
-  return n.M * n.C <= few || (n.C > kNormWide && n.C % 4);
+  return n.M * n.C <= few || (n.C > kNormValues && n.C % 4);
 }
 
 size_t norm_workspace_bytes(const NormCall& n) {
@@ -701,7 +734,7 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
     using T = typename decltype(tag)::type;
     using WT = typename decltype(wtag)::type;
     constexpr bool VEC = decltype(vec)::value;
-    if (norm_few(n) || (!VEC && n.C > kNormWide)) return few(tag, wtag, vec);
+    if (norm_few(n) || (!VEC && n.C > kNormValues)) return few(tag, wtag, vec);
     if constexpr (VEC) {
       if (n.C > 512) {
         using namespace svdq;
@@ -729,15 +762,22 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
         return size(Int<32>(), Int<16>(), Int<1>(), std::false_type());
       }
     }
-    // rows of lanes of a warp, 16 values each in pieces; or 4 single values a thread
-    constexpr int NV = VEC ? 16 / svdq::kVecN<T> : 4, MAXT = VEC ? 256 : 512;
-    const int threads = VEC ? team_lanes((int)n.C) : round_up((int)(n.C + 3) / 4, 32);
-    const dim3 block(threads, std::max(1, VEC ? MAXT / threads : std::min(MAXT / threads, 8)));
-    const size_t smem = (size_t)block.y * n.C * 4;   // at most 16 KB: the teams' values
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = pdl_config((unsigned)(groups * a.chunks), block, smem, st, attr);
-    SVDQ_CUDA(cudaLaunchKernelEx(&cfg, svdq::layernorm_backward_kernel<T, WT, NV, MAXT, VEC>, a));
-    return SVDQ_OK;
+    auto go = [&](auto kern, int threads, int limit) -> svdq_status {
+      const dim3 block(threads, limit / threads);
+      const size_t smem = (size_t)block.y * n.C * 4;   // at most 16 KB: the teams' sums
+      cudaLaunchConfig_t cfg = pdl_config((unsigned)(groups * a.chunks), block, smem, st, attr);
+      SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
+      return SVDQ_OK;
+    };
+    if constexpr (VEC) {   // lanes of a warp, 16 values each
+      return go(svdq::layernorm_backward_kernel<T, WT, 16 / svdq::kVecN<T>, 256>, team_lanes((int)n.C), 256);
+    } else {               // warps, 4 or 8 single values a thread
+      return value_width(n.C, [&](auto nv, auto maxt) {
+        constexpr int MAXT = decltype(maxt)::value;
+        return go(svdq::layernorm_backward_values_kernel<T, WT, decltype(nv)::value, MAXT>, value_lanes(n.C), MAXT);
+      });
+    }
   });
   if (r != SVDQ_OK || !a.part) return r;
   const int64_t cols = groups * C;

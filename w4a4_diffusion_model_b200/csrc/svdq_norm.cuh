@@ -160,11 +160,114 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_kernel(const NormArgs a) {
   }
 }
 
-// (Rows off 16-byte boundaries keep to the kernels above. The ring with copies of
-// the aligned span around each row was built and measured for them: 16384 x 1151
-// bf16 55 against 64 us, 16384 x 3001 181 against 141; single values cost their
-// instructions either way.)
-//
+// Forward for rows off 16-byte boundaries, single values: NV of them a thread, a
+// team of warps per row (blockDim.y teams), blockIdx.x = group * chunks + chunk.
+// Bound: instructions, so weight and bias of the group stay in registers, addresses
+// advance by a row's stride, columns are tested once, and the next row is loaded
+// across the reductions. A warp takes the mean and the squares around it of its own
+// columns; warps are joined behind one barrier as in the kernel below. bf16, one
+// row a block without the next row's loads against this: 16384 x 1151 59 / 34.6 us,
+// 40000 x 777 110 / 64, 16384 x 3001 138 / 95 (a ring with copies of the aligned span
+// around each row: 55 at 1151). Rows loaded ahead of the weights: 38.7 -> 34.6.
+template <typename T, typename WT, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : 3) layernorm_values_kernel(const NormArgs a) {
+  constexpr int W = MAXT / 32;
+  __shared__ float2 slots[2][W];
+  const int tid = threadIdx.x, team = threadIdx.y, teams = blockDim.y, lanes = blockDim.x;
+  const int warps = lanes >> 5;
+  const float inv_c = 1.f / (float)a.C;
+  const long long g = blockIdx.x / a.chunks;
+  const int chunk = (int)(blockIdx.x % a.chunks);
+  const long long row0 = g * a.rows_per_group;
+  const long long rows = min(a.rows_per_group, a.M - row0);
+  const long long step = (long long)a.chunks * teams, first = (long long)chunk * teams;
+  // columns of warp w
+  auto columns = [&](int w) {
+    int n = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) n += min(max(a.C - v * lanes - 32 * w, 0), 32);
+    return (float)n;
+  };
+  const float inv_n = 1.f / columns(tid >> 5);
+  const int joined = tid & (W - 1);   // every W lanes join the team's warps
+  const float joined_n = joined < warps ? columns(joined) : 0.f;
+  bool in[NV];
+  float gain[NV], bias[NV];
+  grid_dependency_wait();
+  grid_launch_dependents();
+#pragma unroll
+  for (int v = 0; v < NV; ++v) in[v] = v * lanes + tid < a.C;
+  long long m = row0 + first + team;
+  const T* x = static_cast<const T*>(a.x) + m * a.ldx + tid;
+  T* y = static_cast<T*>(a.y) + m * a.ldy + tid;
+  T r[NV];
+  auto fetch = [&](bool live) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      r[v] = from_float<T>(0.f);
+      if (live && in[v]) r[v] = x[v * lanes];
+    }
+  };
+  bool live = first + team < rows;
+  fetch(live);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = v * lanes + tid;
+    float w[1] = {0.f}, b[1] = {0.f};
+    if (in[v]) {
+      norm_gain<WT, 1>(a, g, c, w);
+      if (a.b) load_params<WT, 1>(static_cast<const WT*>(a.b) + g * a.C + c, b);
+    }
+    gain[v] = w[0];
+    bias[v] = b[0];
+  }
+  int turn = 0;
+  // every team makes the same number of turns: the reduction has a barrier of the block
+  for (long long k = first; k < rows; k += step, turn ^= 1) {
+    float f[NV], sum = 0.f, sq = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      f[v] = to_float(r[v]);
+      sum += f[v];
+    }
+    const bool store = live;
+    const long long row = m;
+    live = k + step + team < rows;
+    m += step;
+    x += step * a.ldx;
+    fetch(live);
+    float mean = warp_sum(sum) * inv_n;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      if (in[v]) sq = fmaf(f[v] - mean, f[v] - mean, sq);
+    sq = warp_sum(sq);
+    if (warps > 1) {
+      float2* slot = slots[turn] + team * warps;
+      if ((tid & 31) == 0) slot[tid >> 5] = make_float2(mean, sq);
+      __syncthreads();
+      const float2 w = joined < warps ? slot[joined] : make_float2(0.f, 0.f);
+      mean = w.x * joined_n;
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(0xFFFFFFFFu, mean, o);
+      mean *= inv_c;
+      sq = joined < warps ? fmaf((w.x - mean) * (w.x - mean), joined_n, w.y) : 0.f;
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+    }
+    const float rstd = __frsqrt_rn(fmaf(sq, inv_c, a.eps));
+    if (store) {
+      if (tid == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (in[v]) y[v * lanes] = from_float<T>(fmaf((f[v] - mean) * rstd, gain[v], bias[v]));
+    }
+    y += step * a.ldy;
+  }
+}
+
 // Forward for rows of more than one warp, many of them: a block per row, rows
 // streamed through the ring, weight and bias of the group in registers. Thread
 // t holds the pieces t, t + blockDim.x, ... of a row, E elements: 32 of them
@@ -330,18 +433,42 @@ __global__ void __launch_bounds__(32 * W, 16 / W) layernorm_rows_kernel(const No
   if (tid == 0) ring.leave();
 }
 
+// The sums of a block's teams, piece v of thread t at column (v blockDim.x + t) N,
+// added in team order by way of shared memory ([teams][C]) into row g of out.
+template <int NV, int N>
+__device__ __forceinline__ void join_teams(const float (&sum)[NV][N], float* smem, float* out, long long g, int C) {
+  const int tid = threadIdx.x, team = threadIdx.y, teams = blockDim.y;
+  const int threads = blockDim.x * blockDim.y, thread = team * blockDim.x + tid;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * (int)blockDim.x + tid) * N;
+    if (c < C) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) smem[team * C + c + i] = sum[v][i];
+    }
+  }
+  __syncthreads();
+  if (out)
+    for (int c = thread; c < C; c += threads) {
+      float t = smem[c];
+      for (int k = 1; k < teams; ++k) t += smem[k * C + c];
+      out[g * C + c] = t;
+    }
+}
+
 // Backward. blockIdx.x = group * chunks + chunk; a block's teams (blockDim.y of
 // them) take the chunk's rows in turn and add dy xhat and dy of their columns
 // in registers; the block then adds its teams' sums in team order and writes
 // one partial row of dw and db. Every order is fixed, so are the results.
-template <typename T, typename WT, int NV, int MAXT, bool VEC>
+//
+// Rows of up to 512 channels in 16-byte pieces: a team is some lanes of a warp.
+template <typename T, typename WT, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormArgs a) {
-  using P = Piece<T, VEC>;
+  using P = Piece<T, true>;
   constexpr int N = P::kN;
   extern __shared__ float norm_smem[];      // [teams][C]: the teams' sums
-  __shared__ float2 slots[2][32];
   const int tid = threadIdx.x, team = threadIdx.y, teams = blockDim.y;
-  const int warps = blockDim.x >> 5;
   const float inv_c = 1.f / (float)a.C;
   const long long g = blockIdx.x / a.chunks;
   const int chunk = (int)(blockIdx.x % a.chunks);
@@ -356,9 +483,8 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormA
     for (int i = 0; i < N; ++i) dw[v][i] = db[v][i] = 0.f;
   grid_dependency_wait();
   grid_launch_dependents();
-  int turn = 0;
-  // every team makes the same number of turns: the team's reduction has a barrier of the block
-  for (long long k = (long long)chunk * teams; k < rows; k += (long long)a.chunks * teams, turn ^= 1) {
+  // every team makes the same number of turns: its lanes' shuffles take the whole warp
+  for (long long k = (long long)chunk * teams; k < rows; k += (long long)a.chunks * teams) {
     const bool live = k + team < rows;
     const long long m = row0 + (live ? k + team : k);
     const T* x = static_cast<const T*>(a.x) + m * a.ldx;
@@ -399,19 +525,7 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormA
         }
       }
     }
-    float2 s;
-    if (teams == 1 || warps <= 1) {
-      s = team_sum2(s1, s2, slots[turn]);
-    } else {   // several teams of several warps: every warp leaves its sums, a team adds its own
-      s1 = warp_sum(s1);
-      s2 = warp_sum(s2);
-      const int w = team * warps + (tid >> 5), lane = tid & 31;
-      if (lane == 0) slots[turn][w] = make_float2(s1, s2);
-      __syncthreads();
-      const float2 t = lane < warps ? slots[turn][team * warps + lane] : make_float2(0.f, 0.f);
-      s = make_float2(warp_sum(t.x), warp_sum(t.y));
-    }
-    const float m1 = s.x * inv_c, m2 = s.y * inv_c;
+    const float m1 = lanes_sum(s1) * inv_c, m2 = lanes_sum(s2) * inv_c;
     if (live) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -427,30 +541,123 @@ __global__ void __launch_bounds__(MAXT, 1) layernorm_backward_kernel(const NormA
     }
   }
   if (!sums) return;
-  // the teams' sums, added in team order by way of shared memory
-  const long long cols = groups * a.C;
-  const int threads = blockDim.x * blockDim.y, thread = team * blockDim.x + tid;
+  float* const out[2] = {a.part ? a.part + 2ll * chunk * groups * a.C : a.dw,
+                         a.part ? a.part + (2ll * chunk + 1) * groups * a.C : a.db};
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    float* out = which ? a.db : a.dw;
-    if (a.part) out = a.part + (2ll * chunk + which) * cols;
-    __syncthreads();
+  for (int which = 0; which < 2; ++which)
+    join_teams<NV, N>(which ? db : dw, norm_smem, out[which], g, a.C);
+}
+
+// The same for rows off 16-byte boundaries, single values: NV of them a thread, a
+// team of warps per row. Bound: instructions, so addresses advance by a row's
+// stride, columns are tested once, xhat and h stay in registers between the
+// row's sums and its dx, and the next row is loaded across the sums' reduction.
+// bf16, without these against with them: 16384 x 1151 118 / 57.6 us, 40000 x 777
+// 246 / 91, 17060 x 434 57.6 / 25.5.
+template <typename T, typename WT, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, 512 / MAXT) layernorm_backward_values_kernel(const NormArgs a) {
+  extern __shared__ float norm_smem[];      // [teams][C]: the teams' sums
+  __shared__ float2 slots[2][MAXT / 32];
+  const int tid = threadIdx.x, team = threadIdx.y, teams = blockDim.y, lanes = blockDim.x;
+  const int warps = lanes >> 5, lane = tid & 31;
+  const float inv_c = 1.f / (float)a.C;
+  const long long g = blockIdx.x / a.chunks;
+  const int chunk = (int)(blockIdx.x % a.chunks);
+  const long long groups = gridDim.x / a.chunks;
+  const long long row0 = g * a.rows_per_group;
+  const long long rows = min(a.rows_per_group, a.M - row0);
+  const long long step = (long long)a.chunks * teams, first = (long long)chunk * teams;
+  bool in[NV];
+  float gain[NV], dw[NV][1], db[NV][1];
+  grid_dependency_wait();
+  grid_launch_dependents();
+#pragma unroll
+  for (int v = 0; v < NV; ++v) in[v] = v * lanes + tid < a.C;
+  // the team's row and its statistics; rows behind the group's last read as zeros
+  long long m = row0 + first + team;
+  const T* x = static_cast<const T*>(a.x) + m * a.ldx + tid;
+  const T* dy = static_cast<const T*>(a.dy) + m * a.lddy + tid;
+  T* dx = static_cast<T*>(a.dx) + m * a.lddx + tid;
+  T rx[NV], ry[NV];
+  float mean, rstd;
+  auto fetch = [&](bool live) {
+    mean = live ? a.mean[m] : 0.f;
+    rstd = live ? a.rstd[m] : 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = (v * (int)blockDim.x + tid) * N;
-      if (c < a.C) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) norm_smem[team * a.C + c + i] = which ? db[v][i] : dw[v][i];
+      rx[v] = ry[v] = from_float<T>(0.f);
+      if (live && in[v]) {
+        rx[v] = x[v * lanes];
+        ry[v] = dy[v * lanes];
       }
     }
-    __syncthreads();
-    if (out)
-      for (int c = thread; c < a.C; c += threads) {
-        float t = norm_smem[c];
-        for (int k = 1; k < teams; ++k) t += norm_smem[k * a.C + c];
-        out[g * a.C + c] = t;
-      }
+  };
+  bool live = first + team < rows;
+  fetch(live);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = v * lanes + tid;
+    float w[1] = {0.f};
+    if (in[v]) norm_gain<WT, 1>(a, g, c, w);
+    gain[v] = w[0];
+    dw[v][0] = db[v][0] = 0.f;
   }
+  int turn = 0;
+  // every team makes the same number of turns: the reduction has a barrier of the block
+  for (long long k = first; k < rows; k += step, turn ^= 1) {
+    float xh[NV], h[NV], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const float d = to_float(ry[v]);
+      xh[v] = in[v] ? (to_float(rx[v]) - mean) * rstd : 0.f;
+      h[v] = gain[v] * d;
+      dw[v][0] = fmaf(d, xh[v], dw[v][0]);
+      db[v][0] += d;
+      s1 += h[v];
+      s2 = fmaf(h[v], xh[v], s2);
+    }
+    const float row_rstd = rstd;
+    const bool store = live;
+    live = k + step + team < rows;
+    m += step;
+    x += step * a.ldx;
+    dy += step * a.lddy;
+    fetch(live);
+    // both sums at once: the lower lanes reduce s1, the upper ones s2
+    float t = lane < 16 ? s1 : s2;
+    t += __shfl_xor_sync(0xFFFFFFFFu, lane < 16 ? s2 : s1, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    float m1, m2;
+    if (warps == 1) {
+      m1 = __shfl_sync(0xFFFFFFFFu, t, 0);
+      m2 = __shfl_sync(0xFFFFFFFFu, t, 16);
+    } else {
+      float2* slot = slots[turn] + team * warps;
+      if ((lane & 15) == 0) reinterpret_cast<float*>(slot + (tid >> 5))[lane >> 4] = t;
+      __syncthreads();
+      m1 = m2 = 0.f;
+      for (int i = 0; i < warps; ++i) {
+        const float2 w = slot[i];
+        m1 += w.x;
+        m2 += w.y;
+      }
+    }
+    m1 *= inv_c;
+    m2 *= inv_c;
+    if (store) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (in[v]) dx[v * lanes] = from_float<T>(row_rstd * (h[v] - m1 - xh[v] * m2));
+    }
+    dx += step * a.lddx;
+  }
+  if (!a.dw && !a.db) return;
+  float* const out[2] = {a.part ? a.part + 2ll * chunk * groups * a.C : a.dw,
+                         a.part ? a.part + (2ll * chunk + 1) * groups * a.C : a.db};
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+    join_teams<NV, 1>(which ? db : dw, norm_smem, out[which], g, a.C);
 }
 
 // Backward for rows of more than one warp: a block per chunk of a group's rows,
