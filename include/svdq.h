@@ -395,8 +395,9 @@ SVDQ_API svdq_status svdq_int8_layernorm_quantize(int64_t M, int64_t C, int dtyp
  * calls give the same bits), and may each be NULL. mean and rstd are those of
  * the forward pass. M = 0 writes zeros to dweight and dbias [1][C]. dX may be dY
  * or X (with its row stride). The workspace holds partial sums:
- * svdq_layernorm_backward_workspace() bytes, NULL when that is 0 or dweight and
- * dbias are both NULL; it must not be shared by calls that overlap. */
+ * svdq_layernorm_backward_workspace() bytes, which is enough for every type and
+ * stride, NULL when that is 0 or dweight and dbias are both NULL; it must not be
+ * shared by calls that overlap. */
 SVDQ_API svdq_status svdq_layernorm_backward_workspace(int64_t M, int64_t C, int64_t rows_per_group, size_t* bytes);
 SVDQ_API svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype, const void* dY,
                                              int64_t lddy, const void* X, int64_t ldx, const void* weight,

@@ -145,3 +145,22 @@ def test_oracle_codes_are_the_nearest():
         d = np.abs(x[r].astype(np.float64)[:, None] / float(s[r]) - np.arange(-127, 128))
         np.testing.assert_array_equal(q[r], d.argmin(1) - 127)
     assert np.abs(q).max() == 127
+
+
+# rows around the limits of the few-rows form and past them; affine, and groups that share the blocks
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls' pointers are made up: they must end at the missing device")
+@pytest.mark.parametrize("M,rows", [(1, 0), (257, 0), (401, 0), (593, 0), (2000, 0), (70000, 0), (2000, 500), (2000, 7)])
+def test_queried_workspace_serves_every_type_and_layout(lib, M, rows):
+    """The query names neither type nor strides, so its answer has to do for each: 16-bit and fp32 rows of every width,
+    dense and off 16-byte boundaries."""
+    need = ctypes.c_size_t()
+    refused = []
+    for C in range(1, 16385):
+        assert lib.svdq_layernorm_backward_workspace(M, C, rows, ctypes.byref(need)) == 0
+        for dt in (BF, FP16, FP32):
+            for ld in (C, C + 1):
+                status = backward(lib, M=M, C=C, dt=dt, wt=dt, lddy=ld, ld=ld, lddx=ld, rows=rows, dw=GOOD, db=GOOD,
+                                  ws=GOOD if need.value else None, wsb=need.value)
+                if status != NODEV:
+                    refused.append((C, dt, ld, status))
+    assert not refused, f"{len(refused)} calls refused, the first {refused[:3]}"

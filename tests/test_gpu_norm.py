@@ -292,3 +292,35 @@ def test_single_values_nan_and_infinity_stay_in_their_rows(C):
     keep[[7, 500]] = False
     assert torch.equal(Y[keep], Y2[keep]) and torch.equal(dX[keep], dX2[keep])
     assert Y2[~keep].isnan().all() and dX2[~keep].isnan().all()
+
+
+# 16-bit rows of four-value pieces, wider than the forms for single values take, and rows that a stride puts off 16-byte
+# boundaries, at row counts that leave the few-rows limits
+@pytest.mark.parametrize("M,C,dtype", [(700, 5124, BF), (600, 9004, FP16), (410, 16380, BF), (700, 5124, FP32)])
+def test_wide_rows_of_half_pieces(M, C, dtype):
+    run(*case(M, C, dtype, FP32, 2, 6), add_one=True)
+
+
+@pytest.mark.parametrize("M,C,pad,groups", [(500, 64, 0, 1), (700, 381, 0, 2), (700, 1152, 0, 1), (700, 1152, 3, 1),
+                                            (450, 4096, 0, 2), (450, 4096, 1, 2), (420, 5124, 0, 1), (420, 8192, 5, 1)])
+@pytest.mark.parametrize("dtype", [BF, FP32])
+def test_nothing_is_written_past_the_workspace(M, C, pad, groups, dtype):
+    x, w, b, dy = (t.cuda() for t in case(M, C, dtype, FP32, groups, 7))
+    _, mean, rstd = S.svdq_layernorm(x, w, b)
+    want = S.svdq_layernorm_backward(dy, x, w, mean, rstd)
+    X, dY, dX = (torch.empty(M, C + pad, dtype=dtype, device="cuda")[:, :C].copy_(t) for t in (x, dy, x))
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    need = S.svdq_layernorm_backward_workspace(M, C, M // groups)
+    work = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    t = S.DTYPES[dtype]
+    status = S.load().svdq_layernorm_backward(M, C, t, S.DTYPES[FP32], dY.data_ptr(), C + pad, X.data_ptr(), C + pad,
+                                              w.data_ptr(), mean.data_ptr(), rstd.data_ptr(), M // groups, 0,
+                                              dX.data_ptr(), C + pad, dw.data_ptr(), db.data_ptr(), work.data_ptr(), need,
+                                              torch.cuda.current_stream().cuda_stream)
+    assert status == 0 and (work[need:] == 0xA5).all()
+    args = B.np64(dy), B.np64(x), B.np64(w), B.np64(mean), B.np64(rstd), M // groups, False
+    dx, gw, gb, bx, bw, bb = B.layernorm_backward(*args)
+    B.within(dX, dx, bx + B.rounding(dx, dtype), "dX")
+    B.within(dw, gw, bw + B.rounding(gw, FP32), "dweight")
+    B.within(db, gb, bb + B.rounding(gb, FP32), "dbias")
+    assert torch.equal(want[0], dX) or pad

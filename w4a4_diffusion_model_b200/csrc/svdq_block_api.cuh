@@ -412,14 +412,19 @@ int64_t norm_groups(const NormCall& n) {
   return std::max<int64_t>(1, (n.M + rows - 1) / rows);
 }
 
-// Calls f<T, WT, VEC>: 16-byte pieces when the rows, their strides and C allow it.
+// Whether rows of C values with these strides are whole 16-byte pieces.
+bool norm_pieces(const NormCall& n, std::initializer_list<int64_t> strides) {
+  const int64_t piece = 16 / type_bytes(n.dtype);
+  bool vec = n.C % piece == 0;
+  if (n.M > 1)
+    for (int64_t ld : strides) vec = vec && ld % piece == 0;
+  return vec;
+}
+
+// Calls f<T, WT, VEC>.
 template <typename F>
-svdq_status norm_dispatch(const NormCall& n, std::initializer_list<int64_t> strides, F&& f) {
+svdq_status norm_dispatch(const NormCall& n, bool vec, F&& f) {
   return with_type(n.dtype, [&](auto tag) -> svdq_status {
-    using T = typename decltype(tag)::type;
-    bool vec = n.C % svdq::kVecN<T> == 0;
-    if (n.M > 1)
-      for (int64_t ld : strides) vec = vec && ld % svdq::kVecN<T> == 0;
     auto go = [&](auto wtag) -> svdq_status {
       if (vec) return f(tag, wtag, std::true_type());
       return f(tag, wtag, std::false_type());
@@ -459,7 +464,7 @@ svdq_status value_width(int64_t C, F&& f) {
 
 template <bool QUANT>
 svdq_status launch_layernorm(const NormCall& n, svdq::NormArgs a, cudaStream_t st) {
-  return norm_dispatch(n, {a.ldx, QUANT ? (int64_t)0 : (int64_t)a.ldy}, [&](auto tag, auto wtag, auto vec) -> svdq_status {
+  return norm_dispatch(n, norm_pieces(n, {a.ldx, QUANT ? (int64_t)0 : (int64_t)a.ldy}), [&](auto tag, auto wtag, auto vec) -> svdq_status {
     using T = typename decltype(tag)::type;
     using WT = typename decltype(wtag)::type;
     constexpr bool VEC = decltype(vec)::value;
@@ -505,41 +510,62 @@ svdq_status launch_layernorm(const NormCall& n, svdq::NormArgs a, cudaStream_t s
   });
 }
 
-// Row chunks per group of the backward pass, over all groups as many blocks per SM
-// as are resident at once or, in the ring, blocks of about 640 threads in all (16
-// channels a thread). More groups than that: each block takes a group's rows
-// alone, and no partial sums are kept. (Single values: 4 blocks per SM 4133 x 338
-// 14.9 against 11.8 us, 14324 x 571 36.0 against 34.6.)
-int64_t norm_chunks(const NormCall& n) {
+// What serves a backward pass: decided here alone, from the type, the width, the
+// rows and whether these are whole 16-byte pieces, for the workspace query, the
+// check of the workspace and the launch alike.
+enum class NormForm {
+  kFew,      // layernorm_backward_few_kernel: one launch, no workspace
+  kRing,     // layernorm_backward_rows_kernel
+  kLanes,    // layernorm_backward_kernel: a row in some lanes of a warp
+  kValues,   // layernorm_backward_values_kernel: off 16-byte boundaries
+};
+
+struct NormPlan {
+  NormForm form;
+  int64_t chunks;     // row chunks per group
+  size_t workspace;   // bytes of the chunks' partial sums
+};
+
+// kFew for few rows, and for rows too wide for single values in registers: it reads
+// them twice, instead of two launches and partial sums. Measured, us, few against
+// ring (bf16): 32 x 1152 2.7 / 5.6, 226 x 4096 6.2 / 8.1, 226 x 8192 9.3 / 11.8
+// (fp32 13.2 / 12.7), 512 x 2048 6.6 / 6.3, 1024 x 1152 9.6 / 8.2; against single
+// values: 32 x 1151 3.4 / 7.4, 226 x 1151 fp32 4.7 / 7.7, 400 x 691 6.8 / 7.8,
+// 400 x 51 6.2 / 5.2 (one launch and no workspace are 5 us less on the host),
+// 2048 x 3001 38 / 23, 4096 x 1151 68 / 18; 16 values a thread, of 1024, without the
+// next row's loads: 8192 x 8763 333 / 622.
+// Row chunks of the others: over all groups as many blocks per SM as are resident
+// at once or, in the ring, blocks of about 640 threads in all (16 channels a
+// thread). More groups than that: each block takes a group's rows alone, and no
+// partial sums are kept. (Single values: 4 blocks per SM 4133 x 338 14.9 against
+// 11.8 us, 14324 x 571 36.0 against 34.6.)
+NormPlan norm_backward_plan(const NormCall& n, bool pieces) {
+  const int64_t few = n.M <= 256 ? 1ll << 21 : n.M <= 400 ? 1ll << 20 : 0;
+  if (n.M * n.C <= few || (!pieces && n.C > kNormValues)) return NormPlan{NormForm::kFew, 1, 0};
   const int64_t groups = norm_groups(n);
+  NormForm form = NormForm::kLanes;
   int64_t per_sm = 2;
-  if (n.C % (n.dtype == SVDQ_FP32 ? 4 : 8)) {
+  if (!pieces) {
     const int lanes = value_lanes(n.C), limit = value_limit(n.C);
-    if (n.C <= kNormValues) per_sm = 512 / (limit / lanes * lanes);
+    form = NormForm::kValues;
+    per_sm = 512 / (limit / lanes * lanes);
   } else if (n.C > 512) {
+    form = NormForm::kRing;
     per_sm = std::max<int64_t>(1, 640 / round_up((int)(n.C + 15) / 16, 32));
   }
   const int64_t per = std::max<int64_t>(1, per_sm * sm_count() / groups);
-  return std::min<int64_t>(per, std::max<int64_t>(1, (norm_group_rows(n) + 3) / 4));
+  const int64_t chunks = std::min<int64_t>(per, std::max<int64_t>(1, (norm_group_rows(n) + 3) / 4));
+  return NormPlan{form, chunks, chunks == 1 ? 0 : (size_t)(2 * chunks * groups * n.C) * 4u};
 }
 
-// Few rows, and rows too wide for single values in registers: one launch that reads
-// them twice instead of two and partial sums. Measured, us, few against ring
-// (bf16): 32 x 1152 2.7 / 5.6, 226 x 4096 6.2 / 8.1, 226 x 8192 9.3 / 11.8 (fp32
-// 13.2 / 12.7), 512 x 2048 6.6 / 6.3, 1024 x 1152 9.6 / 8.2; against single values:
-// 32 x 1151 3.4 / 7.4, 226 x 1151 fp32 4.7 / 7.7, 400 x 691 6.8 / 7.8, 400 x 51 6.2 /
-// 5.2 (one launch and no workspace are 5 us less on the host), 2048 x 3001 38 / 23,
-// 4096 x 1151 68 / 18; 16 values a thread, of 1024, without the next row's loads:
-// 8192 x 8763 333 / 622.
-bool norm_few(const NormCall& n) {
-  const int64_t few = n.M <= 256 ? 1ll << 21 : n.M <= 400 ? 1ll << 20 : 0;
-  return n.M * n.C <= few || (n.C > kNormValues && n.C % 4);
-}
-
-size_t norm_workspace_bytes(const NormCall& n) {
-  if (norm_few(n)) return 0;
-  const int64_t chunks = norm_chunks(n);
-  return chunks == 1 ? 0 : (size_t)(2 * chunks * norm_groups(n) * n.C) * 4u;
+// The largest workspace over the types and strides that X, dY and dX may have.
+size_t norm_workspace_bytes(NormCall n) {
+  size_t most = 0;
+  for (int dtype : {SVDQ_BF16, SVDQ_FP32}) {   // fp16 is dealt with as bf16
+    n.dtype = n.w_dtype = dtype;
+    for (bool pieces : {false, norm_pieces(n, {})}) most = std::max(most, norm_backward_plan(n, pieces).workspace);
+  }
+  return most;
 }
 
 // Whether two matrices of a norm share memory.
@@ -693,7 +719,9 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
       (r = check_in_place("dX", dX, lddx, X, ldx, M)) != SVDQ_OK)
     return r;
   const bool sums = dweight || dbias;
-  const size_t need = sums ? norm_workspace_bytes(n) : 0;
+  const bool pieces = norm_pieces(n, {lddy, ldx, lddx});
+  const NormPlan plan = norm_backward_plan(n, pieces);
+  const size_t need = sums ? plan.workspace : 0;
   if (need && (!workspace || workspace_bytes < need))
     return fail(SVDQ_ERR_BUFFER_TOO_SMALL, "workspace of %zu bytes, need %zu", workspace ? workspace_bytes : 0, need);
   if ((r = check_device()) != SVDQ_OK) return r;
@@ -708,7 +736,7 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
   a.M = M; a.rows_per_group = norm_group_rows(n); a.C = (int)C;
   a.add = flags & SVDQ_NORM_ADD_ONE ? 1.f : 0.f;
   a.dy = dY; a.lddy = lddy; a.dx = dX; a.lddx = lddx; a.dw = dweight; a.db = dbias;
-  a.chunks = (int)norm_chunks(n);
+  a.chunks = (int)plan.chunks;
   a.part = need ? static_cast<float*>(workspace) : nullptr;
   const int64_t groups = norm_groups(n);
   // The few-rows form, in one launch; dX in the memory of an input: the sums come
@@ -727,16 +755,15 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
       cfg.gridDim = dim3(rows);
       SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
     }
-    a.part = nullptr;   // nothing to join
     return SVDQ_OK;
   };
-  r = norm_dispatch(n, {lddy, ldx, lddx}, [&](auto tag, auto wtag, auto vec) -> svdq_status {
+  r = norm_dispatch(n, pieces, [&](auto tag, auto wtag, auto vec) -> svdq_status {
     using T = typename decltype(tag)::type;
     using WT = typename decltype(wtag)::type;
     constexpr bool VEC = decltype(vec)::value;
-    if (norm_few(n) || (!VEC && n.C > kNormValues)) return few(tag, wtag, vec);
+    if (plan.form == NormForm::kFew) return few(tag, wtag, vec);
     if constexpr (VEC) {
-      if (n.C > 512) {
+      if (plan.form == NormForm::kRing) {
         using namespace svdq;
         const size_t rows = 2 * (size_t)n.C * sizeof(T);
         auto go = [&](auto elems, auto warps, auto blocks, auto hold, auto full) -> svdq_status {
@@ -770,9 +797,9 @@ svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, int w_dtype
       SVDQ_CUDA(cudaLaunchKernelEx(&cfg, kern, a));
       return SVDQ_OK;
     };
-    if constexpr (VEC) {   // lanes of a warp, 16 values each
+    if constexpr (VEC) {   // kLanes: 16 values each
       return go(svdq::layernorm_backward_kernel<T, WT, 16 / svdq::kVecN<T>, 256>, team_lanes((int)n.C), 256);
-    } else {               // warps, 4 or 8 single values a thread
+    } else {               // kValues: warps, 4 or 8 a thread
       return value_width(n.C, [&](auto nv, auto maxt) {
         constexpr int MAXT = decltype(maxt)::value;
         return go(svdq::layernorm_backward_values_kernel<T, WT, decltype(nv)::value, MAXT>, value_lanes(n.C), MAXT);
