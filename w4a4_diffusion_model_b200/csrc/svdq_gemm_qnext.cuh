@@ -126,8 +126,7 @@ __device__ __forceinline__ void epilogue_stage_box(const uint32_t* p, unsigned c
 
 // T' = sum over the N/256 column tiles of their fp32 partials, in tile order,
 // rounded to bf16: ws [slices][M][r], T [M][r]. Four outputs per thread.
-__global__ void __launch_bounds__(256) tprime_reduce_kernel(const float4* __restrict__ ws,
-                                                            __nv_bfloat16* __restrict__ T, long long n4,
+__global__ void __launch_bounds__(256) tprime_reduce_kernel(const float4* ws, __nv_bfloat16* T, long long n4,
                                                             int slices) {
   grid_dependency_wait();     // the GEMM that wrote the partials is complete
   grid_launch_dependents();

@@ -224,8 +224,7 @@ constexpr int kGvThreads = 256;
 constexpr int kGvChannels = 8;
 
 template <int MT, typename OT>
-__global__ void __launch_bounds__(kGvThreads) int8_few_tokens_kernel(const int8_t* __restrict__ qx,
-                                                                     const int8_t* __restrict__ qw,
+__global__ void __launch_bounds__(kGvThreads) int8_few_tokens_kernel(const int8_t* qx, const int8_t* qw,
                                                                      const Int8GemmArgs a, int warps_k) {
   __shared__ int sums[kGvThreads / 32][kGvChannels * MT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

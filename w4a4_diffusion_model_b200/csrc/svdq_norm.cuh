@@ -930,9 +930,8 @@ __global__ void __launch_bounds__(kNormFewThreads) layernorm_backward_few_kernel
 // w adds the chunks w, w + 16, ... in order, then the warps' sums in order.
 constexpr int kPartWarps = 16;
 
-__global__ void __launch_bounds__(32 * kPartWarps) layernorm_partials_kernel(const float* __restrict__ part,
-                                                                 float* __restrict__ dw, float* __restrict__ db,
-                                                                 long long cols, int chunks) {
+__global__ void __launch_bounds__(32 * kPartWarps) layernorm_partials_kernel(const float* part, float* dw, float* db,
+                                                                             long long cols, int chunks) {
   __shared__ float sums[kPartWarps][33];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int which = blockIdx.y;
