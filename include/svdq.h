@@ -358,8 +358,10 @@ SVDQ_API svdq_status svdq_int8_quantize_weight(int64_t N, int64_t K, int w_dtype
 /* Y[m][n] = Sx[m] Sw[n] sum_k Qx[m][k] Qw[n][k] + bias[n]: the integer sum is
  * exact; it is rounded to fp32, multiplied by Sw and then Sx, the bias (fp32
  * [N], or NULL) is added with one rounding, and Y (type y_dtype, row stride
- * ldy >= N) takes the result rounded once. 0 <= M <= 2^30, 1 <= N <= 2^24;
- * codes in [-127, 127] (-128 too); K as above. No workspace. */
+ * ldy >= N) takes the result rounded once. 0 <= M <= 2^30, 1 <= N <= 2^24; K as
+ * above. Codes in [-127, 127], as the quantizers write them; -128 too in Qx or in
+ * Qw, and in both where K < 131072 (at K = 131072 such a sum can be 2^31, which
+ * int32 does not hold). No workspace. */
 SVDQ_API svdq_status svdq_int8_linear(int64_t M, int64_t K, int64_t N, const void* Qx, const float* Sx,
                                       const void* Qw, const float* Sw, const float* bias, int y_dtype, void* Y,
                                       int64_t ldy, void* stream);

@@ -3,6 +3,8 @@ shapes, types, strides, null and misaligned pointers are refused with the
 documented status before a device is touched, and the binding refuses tensors
 that do not fit."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -164,3 +166,15 @@ def test_queried_workspace_serves_every_type_and_layout(lib, M, rows):
                 if status != NODEV:
                     refused.append((C, dt, ld, status))
     assert not refused, f"{len(refused)} calls refused, the first {refused[:3]}"
+
+
+def test_the_documented_codes_cannot_leave_int32(lib):
+    """The extremes that the header allows, against int32's range: -127 to 127 on both sides at the largest K that is
+    taken, -128 on one side, and -128 on both below the K it names."""
+    assert linear(lib, K=131088) == SHAPE
+    with open(os.path.join(B.ROOT, "include", "svdq.h")) as f:
+        text = re.sub(r"\s*\n \*\s*", " ", f.read())
+    both = re.search(r"-128 too in Qx or in Qw, and in both where K < (\d+)", text)
+    assert both, "codes of -128 need a limit on K"
+    assert 127 * 127 * 131072 < 2 ** 31 and 128 * 127 * 131072 < 2 ** 31
+    assert 128 * 128 * (int(both.group(1)) - 16) < 2 ** 31 <= 128 * 128 * int(both.group(1))

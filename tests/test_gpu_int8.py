@@ -252,3 +252,17 @@ def test_replayed_graph_and_other_stream():
         torch.cuda.synchronize()
         assert torch.equal(Y, S.svdq_int8_linear(*S.svdq_int8_quantize_act(X), W))
         assert torch.equal(Z, S.svdq_int8_linear(*S.svdq_int8_quantize_act(other), W))
+
+
+@pytest.mark.parametrize("M,N", [(2, 3), (40, 24), (600, 520)])
+def test_codes_of_minus_128_on_both_sides(M, N):
+    """128 * 128 * 131056 < 2^31, for each kind of kernel; at K = 131072 one side only."""
+    for K, x in ((131056, -128), (131072, -127)):
+        qx = torch.full((M, K), x, dtype=torch.int8, device="cuda")
+        qx[1] = 127
+        qw = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+        W = S.Int8Weights(N, K, qw, torch.ones(N, device="cuda"))
+        Y = S.svdq_int8_linear(qx, torch.ones(M, device="cuda"), W, torch.float32)
+        want = torch.full((M, N), -128.0 * x * K, dtype=torch.float64)
+        want[1] = -128.0 * 127 * K
+        assert torch.equal(Y.cpu(), want.float())

@@ -3,7 +3,7 @@
 //   Y[m][n] = sx[m] sw[n] sum_k qx[m][k] qw[n][k] + bias[n].
 // The integer sum runs on the tensor cores (tcgen05 kind::i8, int32
 // accumulators in tensor memory), so it is exact: |sum| <= 127^2 K < 2^31 for
-// K <= 131072. The epilogue rounds the sum to fp32, multiplies by sw and then by
+// K <= 131072 (128 * 127 K too; 128^2 K is 2^31 at K = 131072). The epilogue rounds the sum to fp32, multiplies by sw and then by
 // sx (in this order: a token's scale may lie anywhere in fp32's range, and the
 // sum times it, or the product of the scales, could leave that range where Y
 // does not), adds the bias in fp32 and rounds once to Y's type.
