@@ -342,7 +342,8 @@ typedef enum { SVDQ_BF16 = 0, SVDQ_FP16 = 1, SVDQ_FP32 = 2, SVDQ_INT32 = 3 } svd
  * one scale per row:
  *   v = fp32(x * inv_lambda[k])   (inv_lambda fp32 [K], or NULL: v = x)
  *   s = fp32(max|v| * fp32(1/127)),  q = clamp(RNE(v / s), -127, 127) of the exact
- *   quotient (ties to even); all 0 if s == 0. A row with an infinity or a NaN
+ *   quotient (ties to even); all 0 if s == 0. (A product, as tensor operations on
+ *   a GPU give it: within 9/16 of a step of max|v| / 127.) A row with an infinity or a NaN
  *   gets the scale NaN and codes 0: what is computed from it is NaN.
  * Writes Qx int8 [M][K] and Sx fp32 [M]. 0 <= M <= 2^30, K a multiple of 16,
  * 16 <= K <= 131072.

@@ -178,3 +178,15 @@ def test_the_documented_codes_cannot_leave_int32(lib):
     assert both, "codes of -128 need a limit on K"
     assert 127 * 127 * 131072 < 2 ** 31 and 128 * 127 * 131072 < 2 ** 31
     assert 128 * 128 * (int(both.group(1)) - 16) < 2 ** 31 <= 128 * 128 * int(both.group(1))
+
+
+def test_the_scale_factor_is_a_sixteenth_of_a_step_off():
+    """fp32(1/127) = (1/127) (1 - 2^-28), in whole numbers; and what the oracle's scales make of it."""
+    c = float(np.float32(1) / np.float32(127))
+    assert 127 * int(c * 2 ** 30) * 2 ** 5 == 2 ** 35 - 2 ** 7 and int(c * 2 ** 30) / 2 ** 30 == c
+    x = np.random.default_rng(3).normal(size=(20000, 16)).astype(np.float32)
+    q, s = O.int8_codes(x)
+    top = np.abs(x.astype(np.float64)).max(1)
+    assert (np.abs(s - top / 127) <= (0.5 + 1 / 16) * np.spacing(s)).all()
+    off = 127 * (2.0 ** -24 + 2.0 ** -28) * (1 + 2.0 ** -20)
+    assert (np.abs(q - 127 * x / top[:, None]) <= 0.5 + off).all()

@@ -266,3 +266,26 @@ def test_codes_of_minus_128_on_both_sides(M, N):
         want = torch.full((M, N), -128.0 * x * K, dtype=torch.float64)
         want[1] = -128.0 * 127 * K
         assert torch.equal(Y.cpu(), want.float())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scales_and_codes_next_to_the_exact_quotients(dtype):
+    """max / 127 in 64 bits: fp32(1/127) is (1/127) (1 - 2^-28), so that the scale is off by half a step and a sixteenth at
+    most, and a code by what that makes of 127 v / max; and the same scales from torch's own division on the GPU."""
+    x = activations(3000, 64, dtype, 21)
+    x *= torch.exp(torch.randn(3000, 1, generator=torch.Generator().manual_seed(22))).to(dtype)
+    x[:2] = 0
+    x[0, 5] = 127.0
+    x[1, 5] = torch.finfo(dtype).tiny
+    X = x.cuda()
+    Q, s = S.svdq_int8_quantize_act(X)
+    v, sc = B.np64(x), B.np64(s)
+    top = np.abs(v).max(1)
+    assert (np.abs(sc - top / 127) <= (0.5 + 1 / 16) * np.spacing(s.cpu().numpy()).astype(np.float64)).all()
+    rounded = (top / 127).astype(np.float32)
+    differ = s.cpu().numpy() != rounded
+    assert (np.abs(sc - rounded)[differ] <= np.spacing(rounded[differ])).all()
+    normal = top / 127 >= np.finfo(np.float32).tiny          # below, a step is more than 2^-23 of the scale
+    off = 127 * (2.0 ** -24 + 2.0 ** -28) * (1 + 2.0 ** -20)
+    assert (np.abs(B.np64(Q.double()) - 127 * v / top[:, None])[normal] <= 0.5 + off).all()
+    assert torch.equal(s, X.float().abs().amax(1) / 127.0)
