@@ -436,15 +436,17 @@ svdq_status norm_dispatch(const NormCall& n, bool vec, F&& f) {
 
 // Threads per row, and f<pieces per thread, limit of the block's threads>: 16
 // values a thread in 16-byte pieces (some lanes of a warp up to 512 values); single
-// values, 4 to 16 a thread (up to kNormValues only for the form that ends in codes).
-template <typename T, bool VEC, typename F>
+// values, 4 to 16 a thread (up to kNormValues only for the form that ends in codes:
+// layernorm_values_kernel has the others).
+template <typename T, bool VEC, bool QUANT, typename F>
 svdq_status norm_width(int C, F&& f) {
   if constexpr (VEC) {
     constexpr int NV = 16 / svdq::kVecN<T>;
     const int threads = C <= 512 ? team_lanes(C) : round_up((C + 15) / 16, 32);
     return threads <= 256 ? f(threads, Int<NV>(), Int<256>()) : f(threads, Int<NV>(), Int<1024>());
   } else {
-    if (C <= 2048) return f(round_up((C + 3) / 4, 32), Int<4>(), Int<512>());
+    if constexpr (QUANT)
+      if (C <= 2048) return f(round_up((C + 3) / 4, 32), Int<4>(), Int<512>());
     if (C <= 8192) return f(round_up((C + 7) / 8, 32), Int<8>(), Int<1024>());
     return f(round_up((C + 15) / 16, 32), Int<16>(), Int<1024>());
   }
@@ -498,7 +500,7 @@ svdq_status launch_layernorm(const NormCall& n, svdq::NormArgs a, cudaStream_t s
           return SVDQ_OK;
         });
     }
-    return norm_width<T, VEC>((int)n.C, [&](int threads, auto nv, auto maxt) -> svdq_status {
+    return norm_width<T, VEC, QUANT>((int)n.C, [&](int threads, auto nv, auto maxt) -> svdq_status {
       constexpr int NV = decltype(nv)::value, MAXT = decltype(maxt)::value;
       const dim3 block(threads, threads <= 32 ? 256 / threads : 1);
       const unsigned grid = (unsigned)std::min<int64_t>((n.M + block.y - 1) / block.y, (int64_t)sm_count() * 16);

@@ -108,19 +108,13 @@ __device__ __forceinline__ void load_params(const WT* p, float (&f)[N]) {
     f[0] = to_float(p[0]);
   } else {
     constexpr int W = kVecN<WT>;
-    static_assert(N % W == 0 || N < W, "parameter vector");
-    if constexpr (N < W) {   // four 16-bit parameters beside four fp32 values
-      const uint2 r = *reinterpret_cast<const uint2*>(p);
-      unpack2(r.x, f[0], f[1], WT());
-      unpack2(r.y, f[2], f[3], WT());
-    } else {
+    static_assert(N % W == 0, "parameter vector");
 #pragma unroll
-      for (int j = 0; j < N / W; ++j) {
-        float t[W];
-        unpack_vec<WT>(*reinterpret_cast<const uint4*>(p + j * W), t);
+    for (int j = 0; j < N / W; ++j) {
+      float t[W];
+      unpack_vec<WT>(*reinterpret_cast<const uint4*>(p + j * W), t);
 #pragma unroll
-        for (int i = 0; i < W; ++i) f[j * W + i] = t[i];
-      }
+      for (int i = 0; i < W; ++i) f[j * W + i] = t[i];
     }
   }
 }
