@@ -324,3 +324,37 @@ def test_nothing_is_written_past_the_workspace(M, C, pad, groups, dtype):
     B.within(dw, gw, bw + B.rounding(gw, FP32), "dweight")
     B.within(db, gb, bb + B.rounding(gb, FP32), "dbias")
     assert torch.equal(want[0], dX) or pad
+
+
+# every width of the forms for single values (strides off 16 bytes) and of whole pieces, one row a block and the ring
+@pytest.mark.parametrize("C", [16, 1152, 4096, 8208, 16384])
+@pytest.mark.parametrize("M,rows", [(7, 4), (400, 150)])
+@pytest.mark.parametrize("dtype,wtype", [(BF, BF), (FP16, FP32), (FP32, FP32)])
+def test_norm_into_codes_of_strided_rows_in_groups(C, M, rows, dtype, wtype):
+    groups = -(-M // rows)
+    x, w, b, _ = case(M, C, dtype, wtype, groups, 8)
+    lam = torch.exp(0.3 * torch.randn(C, generator=torch.Generator().manual_seed(C + 1)))
+    y, _, _, by, _, _ = B.layernorm(B.np64(x), B.np64(w), B.np64(b), 1e-6, rows, True)
+    v, bv = y * B.np64(lam), by * B.np64(lam) + B.U * np.abs(y * B.np64(lam))
+    top, dense = np.abs(v).max(1), None
+    for pad in (0, 16, 3):
+        X = torch.empty(M, C + pad, dtype=dtype, device="cuda")[:, :C].copy_(x)
+        Q, s = S.svdq_int8_layernorm_quantize(X, w.cuda(), b.cuda(), lam.cuda(), rows_per_group=rows, add_one=True)
+        if pad == 16:      # whole pieces all the same: the dense rows' order of sums
+            assert torch.equal(Q, dense[0]) and torch.equal(s, dense[1])
+        dense = dense or (Q, s)
+        B.within(s, top / 127, bv.max(1) / 127 + 2 * B.U * top / 127, "scale")
+        sg = B.np64(s)[:, None]
+        B.within(Q.double(), v / sg, 0.5 + bv / sg + 1e-9, "codes")
+
+
+def test_norm_of_streamed_rows_in_their_own_memory():
+    """Rows that run through the ring, Y over X and strided: the rows ahead are on their way as a row is stored."""
+    for C, pad in ((1024, 0), (4096, 8), (8200, 24)):
+        x, w, b, _ = case(700, C, BF, BF, 2, 9)
+        X = torch.full((700, C + pad), 3.0, dtype=BF, device="cuda")
+        X[:, :C] = x.cuda()
+        Y, mean, rstd = S.svdq_layernorm(X[:, :C], w.cuda(), b.cuda(), add_one=True)
+        got = S.svdq_layernorm(X[:, :C], w.cuda(), b.cuda(), add_one=True, out=X[:, :C])
+        assert torch.equal(X[:, :C], Y) and torch.equal(got[1], mean) and torch.equal(got[2], rstd)
+        assert (X[:, C:] == 3).all()
