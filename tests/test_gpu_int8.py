@@ -289,3 +289,20 @@ def test_scales_and_codes_next_to_the_exact_quotients(dtype):
     off = 127 * (2.0 ** -24 + 2.0 ** -28) * (1 + 2.0 ** -20)
     assert (np.abs(B.np64(Q.double()) - 127 * v / top[:, None])[normal] <= 0.5 + off).all()
     assert torch.equal(s, X.float().abs().amax(1) / 127.0)
+
+
+# rows of Y that end inside a 16-byte piece of a wider matrix whose rows begin on one: pairs whole and in halves of K
+@pytest.mark.parametrize("M,K,N", [(399, 128, 95), (241, 16, 3), (1265, 32, 4), (300, 256, 100), (1100, 8208, 1033),
+                                   (40, 512, 30), (7, 256, 22)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_product_leaves_what_is_behind_its_columns(M, K, N, dtype):
+    piece = 16 // torch.empty(0, dtype=dtype).element_size()
+    ld = N + (-N % piece or piece)
+    check_product(M, K, N, dtype, True, stride=ld)
+    # the last row ends with the memory that belongs to Y
+    size = (M - 1) * ld + N
+    buf = torch.full((size + 4 * piece,), 7.0, dtype=dtype, device="cuda")
+    Y = buf.as_strided((M, N), (ld, 1))
+    W = S.Int8Weights(N, K, torch.ones(N, K, dtype=torch.int8, device="cuda"), torch.ones(N, device="cuda"))
+    S.svdq_int8_linear(torch.ones(M, K, dtype=torch.int8, device="cuda"), torch.ones(M, device="cuda"), W, out=Y)
+    assert (Y == torch.tensor(K, dtype=dtype)).all() and (buf[size:] == 7).all()

@@ -290,7 +290,9 @@ svdq_status launch_int8_pair(const svdq::Int8GemmArgs& a, const void* Qx, const 
                      CU_TENSOR_MAP_SWIZZLE_128B)) != SVDQ_OK)
     return r;
   const uint64_t ld = a.M > 1 ? (uint64_t)a.ldy : (uint64_t)a.N;
-  const bool tma_y = ld * sizeof(OT) % 16 == 0;
+  // Y by TMA where its rows are whole 16-byte pieces: a store writes the last piece of
+  // a row in full, and with it what a wider matrix has behind column N.
+  const bool tma_y = ld * sizeof(OT) % 16 == 0 && a.N * sizeof(OT) % 16 == 0;
   memset(&ty, 0, sizeof(ty));
   if (tma_y && (r = make_tmap(&ty, a.y, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)a.N * sizeof(OT), (uint64_t)a.M,
                               128, 32, CU_TENSOR_MAP_SWIZZLE_128B, ld * sizeof(OT))) != SVDQ_OK)

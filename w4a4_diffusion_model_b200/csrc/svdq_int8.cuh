@@ -631,8 +631,9 @@ __device__ __forceinline__ void int8_store_band(uint32_t taddr, const int* add, 
   }
 }
 
-// tm_y views Y as bytes, in boxes of 32 rows x 128; tma_y = 0 where Y's address or
-// row stride does not allow it (then the staged boxes are written by plain stores).
+// tm_y views Y as bytes, in boxes of 32 rows x 128; tma_y = 0 where Y's rows or their
+// stride are no whole 16-byte pieces (then the staged boxes are written by plain
+// stores).
 //
 // SPLIT: a cluster of two pairs shares one tile, each pair half of K (few tiles and
 // a long K: twice as many SMs work, half as long). Pair p finishes the columns
