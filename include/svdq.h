@@ -423,7 +423,7 @@ SVDQ_API svdq_status svdq_layernorm_backward(int64_t M, int64_t C, int dtype, in
  * with the same strides. positions [pos_rows][axes], int32 or fp32 (pos_dtype),
  * T a multiple of pos_rows (a batch may share its positions); freqs fp64 [R/2]
  * on the device; axis_dims [axes] on the host, each even and >= 2, 1 to 8 axes,
- * R <= D <= 512. Angles are formed and reduced in fp64, so far positions keep
+ * R <= D <= 512, D even, at most 65535 heads. Angles are formed and reduced in fp64, so far positions keep
  * their precision; the turn is in fp32, rounded once. */
 SVDQ_API svdq_status svdq_rope(int64_t T, int32_t heads, int32_t D, int dtype, const void* X, int64_t x_token_stride,
                                int64_t x_head_stride, void* Y, int64_t y_token_stride, int64_t y_head_stride,

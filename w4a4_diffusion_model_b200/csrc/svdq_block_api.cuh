@@ -161,7 +161,7 @@ svdq_status int8_quantize(int64_t M, int64_t K, int dtype, const void* X, int64_
                                               dim3(lanes, teams), st);
     }
     // Many rows: the ring. Measured, us, ring against one row per block: 9001 x
-    // 13824 68 / 105, 4608 x 4096 12.1 / 19; one row per block has the shorter way
+    // 13824 67 / 105, 4608 x 4096 12 / 19; one row per block has the shorter way
     // from memory to registers where rows do not queue.
     if (K <= 16384 && M > 2 * sms) {
       using namespace svdq;
@@ -338,10 +338,10 @@ svdq_status launch_int8_few(const svdq::Int8GemmArgs& a, const void* Qx, const v
 template <typename OT>
 svdq_status launch_int8_linear(const svdq::Int8GemmArgs& a, const void* Qx, const void* Qw, cudaStream_t st) {
   const int64_t weights = (int64_t)a.N * a.K;
-  // Up to 8 tokens: the dot-product kernel costs 2 us + 0.13 (one token), 0.16
-  // (two), 0.21 (four) or 0.37 us (eight) per 2^20 weights; the single-CTA kernel
-  // 21 us at 4096 x 24576 and 8.8 at 4096 x 4096, which eight and four tokens
-  // reach at the sizes below (measured 8.0 us for 8 x 4096 x 4096).
+  // Up to 8 tokens: the dot-product kernel. Measured, us, at 4096 x 4096, 4096 x
+  // 16384 and 4096 x 24576: one token 4.8, 13.5, 19.5; two 6.0, 14.3, 19.7; four 7.7,
+  // 17.6; eight 8.6; the single-CTA kernel (9 tokens, and 5 to 8 from 4096 x 8192 on)
+  // 8.0, 17.4, 21.1, which four and eight tokens reach at the sizes below.
   if (a.M <= 2 || (a.M <= 4 && weights <= (1ll << 26)) || (a.M <= 8 && weights <= (1ll << 24))) {
     if (a.M == 1) return launch_int8_few<1, OT>(a, Qx, Qw, st);
     if (a.M == 2) return launch_int8_few<2, OT>(a, Qx, Qw, st);
@@ -540,7 +540,7 @@ struct NormPlan {
 // next row's loads: 8192 x 8763 333 / 622.
 // Row chunks of the others: over all groups as many blocks per SM as are resident
 // at once or, in the ring, blocks of about 640 threads in all (16 channels a
-// thread). More groups than that: each block takes a group's rows alone, and no
+// thread; at the narrower widths the registers hold 512 of these at a time). More groups than that: each block takes a group's rows alone, and no
 // partial sums are kept. (Single values: 4 blocks per SM 4133 x 338 14.9 against
 // 11.8 us, 14324 x 571 36.0 against 34.6.)
 NormPlan norm_backward_plan(const NormCall& n, bool pieces) {

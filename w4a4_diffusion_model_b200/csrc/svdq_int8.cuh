@@ -218,8 +218,8 @@ struct Int8GemmArgs {
 // rows of W (16 bytes a lane, all loads in flight at once) and the same slice
 // of each token; a block's warps take `warps_k` slices of the same channels in
 // turn, or several channel groups where K is short. Sums are integers, so any
-// order gives the same bits. 2 x 4096 x 24576: 19.7 us, 5.1 TB/s (a 128-row MMA
-// tile 31 us).
+// order gives the same bits. 2 x 4096 x 24576: 19.7 us, 5.1 TB/s (the single-CTA
+// kernel below takes 21.1 for 9 tokens).
 constexpr int kGvThreads = 256;
 constexpr int kGvChannels = 8;
 
@@ -280,10 +280,12 @@ __global__ void __launch_bounds__(kGvThreads) int8_few_tokens_kernel(const int8_
 // ---------------------------------------------------------------- single-CTA kernel
 // One 128 x 256 output tile per CTA and K slice; a cluster of gridDim.z CTAs
 // splits K when there are too few tiles for the GPU. The tile is that wide
-// because an 8-bit integer MMA of 32 K elements takes about 128 cycles whatever
-// its N (measured: 0.28 us per 128 bytes of K for 128 x 64, 128 x 128 and
-// 256 x 256 tiles alike, one accumulator or four), so narrow tiles only repeat
-// it; what shortens a small product is a shorter K slice.
+// because 128 bytes of K cost a CTA 0.28 us whatever the tile (measured over whole
+// kernels: 128 x 64, 128 x 128 and 256 x 256 alike, one accumulator or four), so
+// narrow tiles only repeat it; what shortens a small product is a shorter K slice.
+// For pairs of 256 x 256 that is the tensor peak. For the narrow tiles these times do
+// not tell the MMA's own time from the latency of the loads behind a ring of four
+// stages; nothing here rests on which of the two it is.
 //
 // Warp 0 loads (TMA, 128 bytes of K per stage), warp 1 issues the MMAs, then all
 // eight warps take the accumulator out of tensor memory (warp w: lanes
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kGvThreads) int8_few_tokens_kernel(const int8_
 // writes the columns [z, z + 1) 256 / gridDim.z. A lane keeps its columns and
 // their scales from row to row. Rows past M are neither loaded (the A box is cut
 // to a_rows) nor written, so few tokens cost little traffic. 16 x 4096 x 4096 in
-// quarters of K 8.7 us (pairs 15), 64 x 4096 x 24576 whole 23 us (4.4 TB/s).
+// quarters of K 8.8 us (pairs 15), 64 x 4096 x 24576 whole 23 us (4.4 TB/s).
 constexpr int kI8KTile = 128;                        // K elements (= bytes) per stage row
 constexpr int kI8StageA = 128 * kI8KTile;            // 16 KB
 constexpr int kI8Threads = 256;
