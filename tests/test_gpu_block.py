@@ -171,3 +171,41 @@ def test_tensors_of_one_call_live_on_one_device():
     with pytest.raises(S.SvdqError, match="overlap"):
         S.svdq_rope(torch.randn(4, 2, 16, device="cuda"), torch.zeros(4, 1, dtype=torch.int32, device="cuda"),
                     S.svdq_rope_table((16,)), out=torch.empty(4, 1, 16, device="cuda").expand(4, 2, 16))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in every matrix: the last rows give the bits that they give in a call of their own."""
+    M, C, last, bf16 = 142_008, 15_360, 1000, torch.bfloat16
+    assert (M - last) * C > 2 ** 31
+    x = torch.empty(M, C, dtype=bf16, device="cuda").normal_()
+    w, b = torch.randn(2, C, device="cuda"), torch.randn(2, C, device="cuda")
+    half = M // 2
+    tail = w[1].contiguous(), b[1].contiguous()
+    Y, mean, rstd = S.svdq_layernorm(x, w, b)
+    for a, c in zip((Y, mean, rstd), S.svdq_layernorm(x[-last:], *tail)):
+        assert torch.equal(a[-last:], c)
+    dX, _, db = S.svdq_layernorm_backward(Y, x, w, mean, rstd)
+    dX2, *_ = S.svdq_layernorm_backward(Y[-last:], x[-last:], tail[0], mean[-last:].clone(), rstd[-last:].clone())
+    assert torch.equal(dX[-last:], dX2)
+    want = torch.stack([Y[k * half:(k + 1) * half].sum(0, dtype=torch.float64) for k in (0, 1)])
+    size = torch.stack([Y[k * half:(k + 1) * half].float().abs().sum(0) for k in (0, 1)]).double()
+    # a column's sum passes at most half / 4 + 24 additions in turn
+    assert ((db.double() - want).abs() <= (half / 4 + 24) * B.U * size).all()
+    del Y, dX
+    Q, s = S.svdq_int8_layernorm_quantize(x, w, b)
+    for a, c in zip((Q, s), S.svdq_int8_layernorm_quantize(x[-last:], *tail)):
+        assert torch.equal(a[-last:], c)
+    Q, s = S.svdq_int8_quantize_act(x)
+    for a, c in zip((Q, s), S.svdq_int8_quantize_act(x[-last:])):
+        assert torch.equal(a[-last:], c)
+    del Q
+    W = S.svdq_int8_prepare_weights(torch.randn(C, 64, device="cuda"))
+    Q, s = S.svdq_int8_quantize_act(x[:, :64])
+    S.svdq_int8_linear(Q, s, W, out=x)
+    assert torch.equal(x[-last:], S.svdq_int8_linear(Q[-last:], s[-last:].clone(), W))
+    table, pos = S.svdq_rope_table((16, 16)), torch.arange(M, dtype=torch.int32, device="cuda").view(-1, 1).repeat(1, 2)
+    heads = x.view(M, -1, 64)
+    want = S.svdq_rope(heads[-last:], pos[-last:].contiguous(), table)
+    S.svdq_rope(heads, pos, table, out=heads)
+    assert torch.equal(heads[-last:], want)
+    S.svdq_check()
