@@ -385,6 +385,8 @@ def svdq_deltaquant_encode(X: torch.Tensor, dims: tuple[int, int, int], out: tup
 # ---------------------------------------------------------------- around the 4-bit linear layer
 # W8A8 linear, layer norm and rotary positions. Rows may have a stride; every
 # tensor of a call lives on one CUDA device, which need not be the current one.
+# Parameters, positions, codes and statistics are contiguous, and every address is a
+# multiple of 16 bytes; tensors that are not are refused.
 # As everywhere in this module the calls stand outside autograd: results carry no
 # graph, whatever the inputs require, and gradients come from calls of their own
 # (svdq_layernorm_backward; svdq_rope with inverse=True).
